@@ -71,6 +71,9 @@ typedef enum {
     EXL3_ERR_TIMEOUT = 5      /* a bounded device wait ran out (see exl3_workspace_status) */
 } exl3_status;
 
+/* Element types of the calls that take more than fp16. */
+typedef enum { EXL3_F16 = 0, EXL3_BF16 = 1, EXL3_F32 = 2 } exl3_dtype;
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *exl3_status_string(int status);
 
@@ -335,6 +338,143 @@ exl3_status exl3_udu(const double *h, double *ud, int64_t k, void *workspace, si
 size_t exl3_ldlq_workspace_size(int64_t k, int64_t n, int K);
 exl3_status exl3_ldlq(const float *w, const double *h, uint16_t *trellis, float *w_hat, int64_t k, int64_t n,
                       int K, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * 4-bit microscaled matrices (exl3_mx4_*): a second weight format beside the
+ * trellis, and the only one for activations.  An element is 4 bits (e2m1:
+ * sign, 2 exponent bits, 1 mantissa bit; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6), every 32 elements along a row share a power-of-two scale (e8m0), which
+ * is the OCP microscaling format MXFP4: 4.25 bits per element.  The tensor
+ * cores multiply it directly, so nothing is decoded.
+ *   codes    uint8 [rows][k/2]: the element of even column in the low half of
+ *            its byte.
+ *   scales   uint8 [rows][exl3_mx4_scale_stride(k)]: byte b scales columns
+ *            32b .. 32b+31 by 2^(byte - 127), 255 is NaN; a row is padded to
+ *            16 bytes (the padding is never read as a scale).
+ * k, a multiple of 32 (at most 2^22), runs along the sums of a product: a
+ * layer's weights are stored with one row per OUTPUT channel (n rows of k).
+ * Row counts are 0 .. 2^30; with no rows a call is a no-op.  Types are
+ * exl3_dtype.  Pointers, streams and errors as for the calls above.
+ */
+int64_t exl3_mx4_scale_stride(int64_t k); /* 16 ceil(k / 512); 0 if k is invalid */
+
+/*
+ * exl3_mx4_quantize -- rows of fp16, bf16 or fp32 to codes and scales.
+ *   signs     k fp16 that multiply x's columns, or NULL (the suh of a layer).
+ *   rotate    nonzero: x' = H128(x .* signs)/sqrt(128) per 128 columns first
+ *             (k % 128 == 0), as in exl3_hadamard; both operands of a product
+ *             rotated with the same signs give the unrotated product, with
+ *             outliers spread over their block before the rounding.
+ *   positions NULL, or int32 [rows][topk]: row r is written to each of the
+ *             rows positions[r][j] (exl3_moe_sort's), those outside
+ *             [0, out_rows) are skipped; rows that no position names keep
+ *             what they hold.  A row may be named only once.  Without
+ *             positions topk and out_rows are ignored.
+ * A block's scale is 2^(floor(log2(largest magnitude)) - 2) (exponent at least
+ * -127), elements round to nearest, ties to the even code, magnitudes above 6
+ * scales become 6; a block with an infinity or NaN becomes NaN (scale 255,
+ * codes 0).  Scaling is exact; the rotation runs in fp64, so that no code
+ * depends on an order of summation.
+ */
+exl3_status exl3_mx4_quantize(const void *x, int dtype, const void *signs, int rotate, const int32_t *positions,
+                              int64_t topk, int64_t out_rows, uint8_t *codes, uint8_t *scales, int64_t rows, int64_t k,
+                              void *stream);
+
+/*
+ * exl3_mx4_dequantize -- codes and scales to rows x k fp16, bf16 or fp32
+ * (exact in fp32; one rounding to the type, fp16 overflows to infinity).
+ */
+exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *w, int dtype, int64_t rows,
+                                int64_t k, void *stream);
+
+/*
+ * exl3_mx4_matmul -- y = x . w^T for 4-bit x (m rows) and w (n rows), any m
+ * and n, fp32 accumulation, y m x n fp16 or bf16 (row-major, one rounding).
+ * Few rows are bound by w's bytes, many by the tensor cores; the kernel
+ * splits the work evenly over the SMs and adds split sums in a fixed order,
+ * so results are deterministic.  `workspace` as for exl3_gemm (zero-filled
+ * once; one workspace serves these calls and the calls above in turn), at
+ * least exl3_mx4_matmul_workspace_size bytes (a size that depends on the
+ * current device's SM count).  EXL3_ERR_UNSUPPORTED above 2^31 units of
+ * 128 channels x a token tile x 256 columns.
+ */
+size_t exl3_mx4_matmul_workspace_size(int64_t m, int64_t k, int64_t n);
+exl3_status exl3_mx4_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, void *y,
+                            int dtype, int64_t m, int64_t k, int64_t n, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * exl3_mx4_linear -- a layer with 4-bit weights: x (m x k fp16 or bf16) is
+ * quantised as by exl3_mx4_quantize (signs, rotate) into the workspace and
+ * multiplied as by exl3_mx4_matmul; y has x's type.
+ */
+size_t exl3_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n);
+exl3_status exl3_mx4_linear(const void *x, int dtype, const void *signs, int rotate, const uint8_t *wc,
+                            const uint8_t *ws, void *y, int64_t m, int64_t k, int64_t n, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * exl3_mx4_matmul_experts -- a product per expert in one launch: rows
+ * [offsets[e], offsets[e + 1]) of x with expert e's n rows of w.
+ *   offsets  int32 [experts + 1] in DEVICE memory (exl3_moe_sort's): the host
+ *            never learns the experts' row counts.  They must not decrease;
+ *            values outside [0, rows] are taken to its ends.
+ *   xc, xs   rows x k; wc, ws  experts x n x k; y  rows x n fp16 or bf16.
+ *            Rows of y from offsets[experts] on keep what they hold.
+ *   experts  1 .. 1024 (experts * n <= 2^30).
+ * Otherwise as exl3_mx4_matmul.
+ */
+size_t exl3_mx4_matmul_experts_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts);
+exl3_status exl3_mx4_matmul_experts(const uint8_t *xc, const uint8_t *xs, const int32_t *offsets, const uint8_t *wc,
+                                    const uint8_t *ws, void *y, int dtype, int64_t rows, int64_t k, int64_t n,
+                                    int64_t experts, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * exl3_moe_sort -- the order of tokens by expert (a stable counting sort).
+ *   ids        int32 [tokens][topk]: the experts of each token; a choice
+ *              outside [0, experts) has no row (a padding token's -1, say).
+ *   offsets    int32 [experts + 1] (output): expert e's rows are
+ *              [offsets[e], offsets[e + 1]).
+ *   positions  int32 [tokens][topk] (output): the row of each choice, rows of
+ *              one expert in the order of (token, choice); -1 for none.
+ *   tokens 0 .. 2^24, topk 1 .. 1024, tokens * topk < 2^31, experts 1 .. 1024.
+ * `workspace`: at least exl3_moe_sort_workspace_size bytes; its first 64 KiB
+ * are not touched, so a matmul workspace can serve.
+ */
+size_t exl3_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts);
+exl3_status exl3_moe_sort(const int32_t *ids, int64_t tokens, int64_t topk, int64_t experts, int32_t *offsets,
+                          int32_t *positions, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * exl3_moe_gather -- tokens into that order: xs[positions[t][j]] = x[t], for
+ * x tokens x h and xs rows x h of one type.  Positions outside [0, rows) are
+ * skipped, rows that no position names keep what they hold, and a row may be
+ * named only once.  Its gradient is exl3_moe_combine without weights.
+ */
+exl3_status exl3_moe_gather(const void *x, int dtype, const int32_t *positions, int64_t tokens, int64_t topk,
+                            int64_t h, int64_t rows, void *xs, void *stream);
+
+/*
+ * exl3_moe_combine -- rows back to their tokens:
+ *   y[t] = sum over j of weights[t][j] ys[positions[t][j]],
+ * for ys rows x h and y tokens x h of one type, weights fp32 [tokens][topk] or
+ * NULL (all ones).  fp32 sums in the order of j, one rounding; choices whose
+ * position lies outside [0, rows) add nothing (a token without any gets 0).
+ */
+exl3_status exl3_moe_combine(const void *ys, int dtype, const int32_t *positions, const float *weights,
+                             int64_t tokens, int64_t topk, int64_t h, int64_t rows, void *y, void *stream);
+
+/*
+ * exl3_moe_combine_grad -- the gradients of exl3_moe_combine:
+ *   dys[positions[t][j]] = weights[t][j] dy[t]   (rows that no position names
+ *                                                 keep what they hold)
+ *   dweights[t][j] = <dy[t], ys[positions[t][j]]> in fp32 (0 without a row).
+ * dys or dweights may be NULL (not both); ys is read only for dweights.  A
+ * row may be named only once.
+ */
+exl3_status exl3_moe_combine_grad(const void *dy, const void *ys, int dtype, const int32_t *positions,
+                                  const float *weights, int64_t tokens, int64_t topk, int64_t h, int64_t rows,
+                                  void *dys, float *dweights, void *stream);
 
 /*
  * Launch options, process-wide (default 0).

@@ -1,0 +1,367 @@
+// mx4.cu -- exl3_mx4_quantize and exl3_mx4_dequantize: the 4-bit microscaled
+// format (mx4.cuh) from fp16/bf16/fp32 rows and back.
+//
+// Quantisation of 32 values v (after x' = H128(x .* signs)/sqrt(128) if asked
+// for): e = floor(log2(max |v|)) - 2, clamped to [-127, 127], so that the
+// largest magnitude lies in [4, 8) 2^e; each code is v 2^-e rounded to the
+// nearest code, ties to the even one, magnitudes over 6 taken to 6.  A block
+// that holds an infinity or a NaN gets the scale byte 255 and codes 0.
+//
+// A thread takes 8 consecutive columns, 4 threads a block of 32, 16 threads a
+// rotation block of 128.  The scaling by a power of two is exact, so without
+// the rotation every code is the definition's.  With it the sums run in fp64:
+// a rotated value that fp32 sums put on the other side of a rounding border
+// would be off by a whole step of the format, and two code paths (or two
+// split orders) would then disagree by that step.  fp64 sums of 128 fp16
+// values are exact, those of bf16 and fp32 values to 2^-46 of the largest.
+#include "dtypes.cuh"
+#include "exl3_device.cuh"
+#include "exl3_host.h"
+#include "mx4.cuh"
+
+namespace exl3 {
+
+// 8 consecutive elements.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        unpack16<T>(*reinterpret_cast<const uint4 *>(p), v);
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+
+// Codes of 8 scaled values, the first in the lowest 4 bits (round to nearest
+// even, saturating).
+__device__ __forceinline__ uint32_t codes8(const float (&r)[8])
+{
+    uint32_t out;
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+        : "=r"(out)
+        : "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]));
+    return out;
+}
+
+// The scale byte for a block whose largest magnitude has fp64 bits `bits`.
+__device__ __forceinline__ int scale_byte64(uint64_t bits)
+{
+    const int e = (int)(bits >> 52);  // the sign is clear
+    if (e == 2047)
+        return 255;
+    const int b = e - 1023 - 2 + 127;
+    return b < 0 ? 0 : (b > 254 ? 254 : b);
+}
+
+__device__ __forceinline__ int scale_byte32(uint32_t bits)
+{
+    const int e = (int)(bits >> 23);
+    if (e == 255)
+        return 255;
+    return e < 2 ? 0 : e - 2;
+}
+
+// 2^(127 - byte) as fp32 (byte 254 gives the subnormal 2^-127).
+__device__ __forceinline__ float inverse_scale32(int byte)
+{
+    return byte >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+// A double as the fp32 value that rounds to 4 bits the same way: truncated,
+// with the last bit set if anything was cut off, so that a value beside a
+// border or a tie stays beside it.
+__device__ __forceinline__ float sticky32(double v)
+{
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Codes and scale byte of this thread's 8 columns of a block of 32 (4 lanes).
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int *byte)
+{
+    uint32_t top = 0;  // magnitudes order like their bits, NaN above infinity
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int b = scale_byte32(top);
+    *byte = b;
+    if (b == 255)
+        return 0u;
+    const float inv = inverse_scale32(b);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = v[i] * inv;
+    return codes8(r);
+}
+
+__device__ __forceinline__ uint32_t quantize8(const double (&v)[8], int *byte)
+{
+    uint64_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t a = (uint64_t)__double_as_longlong(v[i]) & 0x7fffffffffffffffull;
+        top = a > top ? a : top;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, (unsigned long long)top, d);
+        top = o > top ? o : top;
+    }
+    const int b = scale_byte64(top);
+    *byte = b;
+    if (b == 255)
+        return 0u;
+    const double inv = __longlong_as_double((long long)(1023 + 127 - b) << 52);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = sticky32(v[i] * inv);
+    return codes8(r);
+}
+
+// x' of this thread's 8 columns: the 128-point Hadamard over 16 lanes, three
+// stages in registers and four across lanes.
+__device__ __forceinline__ void rotate8(double (&v)[8])
+{
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & h) == 0) {
+                const double a = v[i], b = v[i + h];
+                v[i] = a + b;
+                v[i + h] = a - b;
+            }
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const bool upper = (threadIdx.x & m) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double o = __shfl_xor_sync(0xffffffffu, v[i], m);
+            v[i] = upper ? o - v[i] : v[i] + o;
+        }
+    }
+    const double s = 0.088388347648318440550;  // 1/sqrt(128)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] *= s;
+}
+
+struct Mx4QuantParams {
+    const void *x;
+    const __half *signs;
+    const int32_t *positions;  // row r goes to rows positions[r topk ..] (null: to row r)
+    uint8_t *codes, *scales;
+    int64_t rows, out_rows;
+    int groups;                // k / 8: threads per row
+    int topk, stride;          // stride: bytes of a row of scales
+};
+
+// A warp takes 32 consecutive groups of 8 columns of the matrix read as one
+// long row; the 4 (or 16) threads of a block never straddle two rows, since
+// a row is a multiple of 32 (128 with ROT) columns.
+template <typename T, bool ROT>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams p)
+{
+    grid_dep_wait();
+    const int64_t total = p.rows * p.groups;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    // rounded up to whole warps: every lane takes part in the shuffles
+    for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x - (threadIdx.x & 31); g0 < total; g0 += stride) {
+        const int64_t g = g0 + (threadIdx.x & 31);
+        const bool live = g < total;
+        const int64_t row = live ? g / p.groups : 0;
+        const int c = live ? (int)(g - row * p.groups) : 0;
+        float v[8];
+        load8<T>((const T *)p.x + (row * p.groups + c) * 8, v);
+        int byte;
+        uint32_t code;
+        if constexpr (ROT) {
+            double d[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] = (double)v[i];
+            if (p.signs) {
+                float s[8];
+                load8<__half>(p.signs + c * 8, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[i] *= (double)s[i];
+            }
+            rotate8(d);
+            code = quantize8(d, &byte);
+        } else {
+            if (p.signs) {
+                float s[8];
+                load8<__half>(p.signs + c * 8, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] *= s[i];
+            }
+            code = quantize8(v, &byte);
+        }
+        if (!live)
+            continue;
+        const int n = p.positions ? p.topk : 1;
+        for (int j = 0; j < n; ++j) {
+            int64_t to = row;
+            if (p.positions) {
+                to = p.positions[row * p.topk + j];
+                if (to < 0 || to >= p.out_rows)
+                    continue;
+            }
+            reinterpret_cast<uint32_t *>(p.codes)[to * p.groups + c] = code;
+            if ((c & 3) == 0) {
+                uint8_t *sc = p.scales + to * p.stride + (c >> 2);
+                *sc = (uint8_t)byte;
+                if (c + 4 == p.groups)  // the row's last block: the unused bytes behind it
+                    for (int i = (c >> 2) + 1; i < p.stride; ++i)
+                        *++sc = 0;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ dequantise ---
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *__restrict__ codes,
+                                                             const uint8_t *__restrict__ scales, int64_t rows,
+                                                             int groups, int stride, T *__restrict__ w)
+{
+    grid_dep_wait();
+    const int64_t total = rows * groups;
+    for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < total; g += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = g / groups;
+        const int c = (int)(g - row * groups);
+        const uint32_t code = codes[g];
+        const int b = scales[row * stride + (c >> 2)];
+        const float s = b == 255 ? __uint_as_float(0x7fc00000u)
+                                 : (b ? __uint_as_float((uint32_t)b << 23) : __uint_as_float(0x00400000u));
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t q = (code >> (4 * i)) & 15u;
+            // exponent 0: mantissa/2; else (1 + mantissa/2) 2^(exponent - 1)
+            const uint32_t ex = (q >> 1) & 3u, man = q & 1u;
+            const float mag = ex ? __uint_as_float(((126u + ex) << 23) | (man << 22)) : 0.5f * (float)man;
+            v[i] = ((q & 8u) ? -mag : mag) * s;
+        }
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4 *>(w + g * 8) = pack16<T>(v);
+        } else {
+            *reinterpret_cast<float4 *>(w + g * 8) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(w + g * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+static unsigned mx4_grid(int64_t threads)
+{
+    const int64_t blocks = (threads + 255) / 256;
+    return (unsigned)(blocks < 148 * 32 ? blocks : 148 * 32);
+}
+
+template <typename T>
+static exl3_status launch_quantize(const Mx4QuantParams &p, bool rotate, cudaStream_t s)
+{
+    auto kern = rotate ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>;
+    if (launch_kernel(kern, dim3(mx4_grid(p.rows * p.groups)), dim3(256), 0, s, p) != cudaSuccess)
+        return EXL3_ERR_CUDA;
+    return launch_status();
+}
+
+}  // namespace exl3
+
+extern "C" int64_t exl3_mx4_scale_stride(int64_t k)
+{
+    return exl3::valid_mx4_k(k) ? exl3::mx4_scale_stride(k) : 0;
+}
+
+extern "C" exl3_status exl3_mx4_quantize(const void *x, int dtype, const void *signs, int rotate,
+                                         const int32_t *positions, int64_t topk, int64_t out_rows, uint8_t *codes,
+                                         uint8_t *scales, int64_t rows, int64_t k, void *stream)
+{
+    using namespace exl3;
+    if (!valid_mx4_k(k) || !valid_mx4_rows(rows) || (rotate && k % 128) ||
+        (dtype != EXL3_F16 && dtype != EXL3_BF16 && dtype != EXL3_F32))
+        return EXL3_ERR_INVALID_ARG;
+    if (positions && (topk < 1 || topk > 1024 || !valid_mx4_rows(out_rows) || !aligned16(positions)))
+        return EXL3_ERR_INVALID_ARG;
+    const int64_t to_rows = positions ? out_rows : rows;
+    if (rows == 0 || to_rows == 0)
+        return EXL3_OK;
+    if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales) ||
+        (signs && !aligned16(signs)))
+        return EXL3_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * (size_t)k * (dtype == EXL3_F32 ? 4 : 2);
+    const size_t cb = (size_t)to_rows * (size_t)(k / 2), sb = (size_t)(to_rows * mx4_scale_stride(k));
+    const void *in[3] = {x, signs, positions};
+    const size_t in_bytes[3] = {xb, (size_t)k * 2, (size_t)rows * (size_t)topk * 4};
+    for (int i = 0; i < 3; ++i)
+        if (in[i] && (ranges_overlap(in[i], in_bytes[i], codes, cb) || ranges_overlap(in[i], in_bytes[i], scales, sb)))
+            return EXL3_ERR_INVALID_ARG;
+    if (ranges_overlap(codes, cb, scales, sb))
+        return EXL3_ERR_INVALID_ARG;
+    Mx4QuantParams p;
+    p.x = x;
+    p.signs = (const __half *)signs;
+    p.positions = positions;
+    p.codes = codes;
+    p.scales = scales;
+    p.rows = rows;
+    p.out_rows = to_rows;
+    p.groups = (int)(k / 8);
+    p.topk = positions ? (int)topk : 1;
+    p.stride = (int)mx4_scale_stride(k);
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (dtype) {
+    case EXL3_F16: return launch_quantize<__half>(p, rotate != 0, s);
+    case EXL3_BF16: return launch_quantize<__nv_bfloat16>(p, rotate != 0, s);
+    default: return launch_quantize<float>(p, rotate != 0, s);
+    }
+}
+
+extern "C" exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *w, int dtype,
+                                           int64_t rows, int64_t k, void *stream)
+{
+    using namespace exl3;
+    if (!valid_mx4_k(k) || !valid_mx4_rows(rows) || (dtype != EXL3_F16 && dtype != EXL3_BF16 && dtype != EXL3_F32))
+        return EXL3_ERR_INVALID_ARG;
+    if (rows == 0)
+        return EXL3_OK;
+    if (!w || !codes || !scales || !aligned16(w) || !aligned16(codes) || !aligned16(scales))
+        return EXL3_ERR_INVALID_ARG;
+    const size_t wb = (size_t)rows * (size_t)k * (dtype == EXL3_F32 ? 4 : 2);
+    if (ranges_overlap(codes, (size_t)rows * (size_t)(k / 2), w, wb) ||
+        ranges_overlap(scales, (size_t)(rows * mx4_scale_stride(k)), w, wb))
+        return EXL3_ERR_INVALID_ARG;
+    const int groups = (int)(k / 8), stride = (int)mx4_scale_stride(k);
+    const dim3 grid(mx4_grid(rows * groups)), block(256);
+    cudaStream_t s = (cudaStream_t)stream;
+    const uint32_t *c = (const uint32_t *)codes;
+    cudaError_t e;
+    switch (dtype) {
+    case EXL3_F16:
+        e = launch_kernel(mx4_dequantize_kernel<__half>, grid, block, 0, s, c, scales, rows, groups, stride, (__half *)w);
+        break;
+    case EXL3_BF16:
+        e = launch_kernel(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, s, c, scales, rows, groups, stride,
+                          (__nv_bfloat16 *)w);
+        break;
+    default:
+        e = launch_kernel(mx4_dequantize_kernel<float>, grid, block, 0, s, c, scales, rows, groups, stride, (float *)w);
+    }
+    return e == cudaSuccess ? launch_status() : EXL3_ERR_CUDA;
+}

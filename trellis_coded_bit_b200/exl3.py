@@ -33,7 +33,16 @@ EXPORTED = ["exl3_status_string", "exl3_version", "exl3_hadamard", "exl3_decode_
             "exl3_workspace_status", "exl3_set_launch_flags", "exl3_launch_flags",
             "exl3_debug_set_wait_limit_ns", "exl3_debug_wait_limit_ns"]
 
+EXPORTED += ["exl3_mx4_scale_stride", "exl3_mx4_quantize", "exl3_mx4_dequantize",
+             "exl3_mx4_matmul_workspace_size", "exl3_mx4_matmul", "exl3_mx4_linear_workspace_size",
+             "exl3_mx4_linear", "exl3_mx4_matmul_experts_workspace_size", "exl3_mx4_matmul_experts",
+             "exl3_moe_sort_workspace_size", "exl3_moe_sort", "exl3_moe_gather", "exl3_moe_combine",
+             "exl3_moe_combine_grad"]
+
 EXL3_LAUNCH_PDL = 1
+
+# exl3_dtype
+DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 _lib = None
 _lock = threading.Lock()
@@ -103,6 +112,26 @@ def load(build_if_needed=True):
         lib.exl3_ldlq_workspace_size.restype = sz
         lib.exl3_ldlq.argtypes = [vp, vp, vp, vp, i64, i64, ci, vp, sz, vp]
         lib.exl3_ldlq.restype = ci
+        lib.exl3_mx4_scale_stride.argtypes = [i64]
+        lib.exl3_mx4_scale_stride.restype = i64
+        lib.exl3_mx4_quantize.argtypes = [vp, ci, vp, ci, vp, i64, i64, vp, vp, i64, i64, vp]
+        lib.exl3_mx4_dequantize.argtypes = [vp, vp, vp, ci, i64, i64, vp]
+        lib.exl3_mx4_matmul_workspace_size.argtypes = [i64, i64, i64]
+        lib.exl3_mx4_matmul.argtypes = [vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, sz, vp]
+        lib.exl3_mx4_linear_workspace_size.argtypes = [i64, i64, i64]
+        lib.exl3_mx4_linear.argtypes = [vp, ci, vp, ci, vp, vp, vp, i64, i64, i64, vp, sz, vp]
+        lib.exl3_mx4_matmul_experts_workspace_size.argtypes = [i64, i64, i64, i64]
+        lib.exl3_mx4_matmul_experts.argtypes = [vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, i64, vp, sz, vp]
+        lib.exl3_moe_sort_workspace_size.argtypes = [i64, i64, i64]
+        lib.exl3_moe_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, sz, vp]
+        lib.exl3_moe_gather.argtypes = [vp, ci, vp, i64, i64, i64, i64, vp, vp]
+        lib.exl3_moe_combine.argtypes = [vp, ci, vp, vp, i64, i64, i64, i64, vp, vp]
+        lib.exl3_moe_combine_grad.argtypes = [vp, vp, ci, vp, vp, i64, i64, i64, i64, vp, vp, vp]
+        for name in ("mx4_matmul", "mx4_linear", "mx4_matmul_experts", "moe_sort"):
+            getattr(lib, "exl3_%s_workspace_size" % name).restype = sz
+        for name in ("mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "mx4_matmul_experts",
+                     "moe_sort", "moe_gather", "moe_combine", "moe_combine_grad"):
+            getattr(lib, "exl3_" + name).restype = ci
         lib.exl3_workspace_status.argtypes = [vp, sz, ci, vp]
         lib.exl3_workspace_status.restype = ci
         lib.exl3_set_launch_flags.argtypes = [ctypes.c_uint]
@@ -399,6 +428,260 @@ def exl3_ldlq(w, h, K, trellis=None, w_hat=None, workspace=None, stream=None):
                             int(K), _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
            "exl3_ldlq")
     return trellis, w_hat
+
+
+# ------------------------------------------- 4-bit matrices and experts ---
+
+def _typed(t, name, types=DTYPES):
+    """Pointer and exl3_dtype of a tensor of one of `types`."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in types:
+        raise TypeError("%s must be a CUDA tensor of %s" % (name, " or ".join(str(d) for d in types)))
+    return _dev(t, t.dtype, name), DTYPES[t.dtype]
+
+
+_HALF_TYPES = (torch.float16, torch.bfloat16)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, is %s" % (name, " x ".join(str(s) for s in shape), tuple(t.shape)))
+
+
+def _output(t, shape, dtype, like, name):
+    """The given output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _shape(t, shape, name)
+    return t
+
+
+def _same_device(*tensors):
+    """The one device of a call's tensors (None entries are skipped)."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("tensors of one call must be on one device, got %s" % sorted(str(d) for d in devices))
+    return devices.pop()
+
+
+def _call(name, device, stream, args):
+    """Calls the library with `device` current, on `stream` or its current stream."""
+    with torch.cuda.device(device):
+        _check(getattr(load(), name)(*args, _stream(stream)), name)
+
+
+def _workspace(t, name):
+    if t is None:
+        raise ValueError("%s needs a workspace (see new_workspace / %s_workspace_size)" % (name, name))
+    return _dev(t, torch.uint8, "workspace")
+
+
+def exl3_mx4_scale_stride(k):
+    """Bytes of a row of scales of a 4-bit matrix with k columns."""
+    return int(load().exl3_mx4_scale_stride(k))
+
+
+def _mx4_operand(codes, scales, dims, what):
+    """Checks a 4-bit operand of `dims` leading dimensions; returns (shape[:-1], k)."""
+    if codes.dim() != dims + 1:
+        raise ValueError("%s codes must have %d dimensions" % (what, dims + 1))
+    k = codes.shape[-1] * 2
+    stride = exl3_mx4_scale_stride(k)
+    if stride == 0:
+        raise ValueError("%s: k = %d must be a positive multiple of 32" % (what, k))
+    _shape(scales, tuple(codes.shape[:-1]) + (stride,), what + " scales")
+    return tuple(codes.shape[:-1]), k
+
+
+def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None, codes=None, scales=None,
+                      stream=None):
+    """Rows x k (fp16, bf16, fp32) to 4-bit codes [rows, k/2] and scales
+    [rows, exl3_mx4_scale_stride(k)] (uint8), optionally behind the signs and
+    the 128-point rotation.  With `positions` (int32 [rows, topk], from
+    exl3_moe_sort) row r goes to each of the rows positions[r] of `out_rows`."""
+    if x.dim() != 2:
+        raise ValueError("x must be rows x k")
+    rows, k = x.shape
+    px, dtype = _typed(x, "x")
+    stride = exl3_mx4_scale_stride(k)
+    if stride == 0:
+        raise ValueError("k = %d must be a positive multiple of 32" % k)
+    if signs is not None:
+        _shape(signs, (k,), "signs")
+    topk, to = 1, rows
+    if positions is not None:
+        if positions.dim() != 2 or positions.shape[0] != rows:
+            raise ValueError("positions must be rows x topk")
+        topk = positions.shape[1]
+        if out_rows is None:
+            raise ValueError("positions need out_rows")
+        to = int(out_rows)
+    codes = _output(codes, (to, k // 2), torch.uint8, x, "codes")
+    scales = _output(scales, (to, stride), torch.uint8, x, "scales")
+    device = _same_device(x, signs, positions, codes, scales)
+    _call("exl3_mx4_quantize", device, stream,
+          (px, dtype, _ptr_or_none(signs, torch.float16, "signs"), 1 if rotate else 0,
+           _ptr_or_none(positions, torch.int32, "positions"), topk, to, _dev(codes, torch.uint8, "codes"),
+           _dev(scales, torch.uint8, "scales"), rows, k))
+    return codes, scales
+
+
+def exl3_mx4_dequantize(codes, scales, dtype=torch.float16, out=None, stream=None):
+    """The values of a 4-bit matrix, rows x k, as fp16, bf16 or fp32."""
+    (rows,), k = _mx4_operand(codes, scales, 1, "matrix")
+    out = _output(out, (rows, k), dtype, codes, "out")
+    po, dt = _typed(out, "out")
+    device = _same_device(codes, scales, out)
+    _call("exl3_mx4_dequantize", device, stream,
+          (_dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales"), po, dt, rows, k))
+    return out
+
+
+def exl3_mx4_matmul_workspace_size(m, k, n):
+    return int(load().exl3_mx4_matmul_workspace_size(m, k, n))
+
+
+def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None, stream=None):
+    """y = x . w^T of two 4-bit matrices (m rows and n rows of k), fp16 or bf16."""
+    (m,), k = _mx4_operand(xc, xs, 1, "x")
+    (n,), kw = _mx4_operand(wc, ws, 1, "w")
+    if kw != k:
+        raise ValueError("x has k = %d, w has %d" % (k, kw))
+    y = _output(y, (m, n), dtype, xc, "y")
+    py, dt = _typed(y, "y", _HALF_TYPES)
+    pw = _workspace(workspace, "exl3_mx4_matmul")
+    device = _same_device(xc, xs, wc, ws, y, workspace)
+    _call("exl3_mx4_matmul", device, stream,
+          (_dev(xc, torch.uint8, "x codes"), _dev(xs, torch.uint8, "x scales"), _dev(wc, torch.uint8, "w codes"),
+           _dev(ws, torch.uint8, "w scales"), py, dt, m, k, n, pw, workspace.numel()))
+    return y
+
+
+def exl3_mx4_linear_workspace_size(m, k, n):
+    return int(load().exl3_mx4_linear_workspace_size(m, k, n))
+
+
+def exl3_mx4_linear(x, wc, ws, signs=None, rotate=False, y=None, workspace=None, stream=None):
+    """A layer with 4-bit weights (n rows of k): x (m x k, fp16 or bf16) is
+    quantised as by exl3_mx4_quantize, then multiplied; y has x's type."""
+    if x.dim() != 2:
+        raise ValueError("x must be m x k")
+    m, k = x.shape
+    px, dt = _typed(x, "x", _HALF_TYPES)
+    (n,), kw = _mx4_operand(wc, ws, 1, "w")
+    if kw != k:
+        raise ValueError("x has k = %d, w has %d" % (k, kw))
+    if signs is not None:
+        _shape(signs, (k,), "signs")
+    y = _output(y, (m, n), x.dtype, x, "y")
+    pw = _workspace(workspace, "exl3_mx4_linear")
+    device = _same_device(x, signs, wc, ws, y, workspace)
+    _call("exl3_mx4_linear", device, stream,
+          (px, dt, _ptr_or_none(signs, torch.float16, "signs"), 1 if rotate else 0, _dev(wc, torch.uint8, "w codes"),
+           _dev(ws, torch.uint8, "w scales"), _dev(y, x.dtype, "y"), m, k, n, pw, workspace.numel()))
+    return y
+
+
+def exl3_mx4_matmul_experts_workspace_size(rows, k, n, experts):
+    return int(load().exl3_mx4_matmul_experts_workspace_size(rows, k, n, experts))
+
+
+def exl3_mx4_matmul_experts(xc, xs, offsets, wc, ws, dtype=torch.float16, y=None, workspace=None, stream=None):
+    """Rows [offsets[e], offsets[e + 1]) of x times expert e's weights, for
+    wc [experts, n, k/2]: y rows x n (rows behind offsets[experts] are not written)."""
+    (rows,), k = _mx4_operand(xc, xs, 1, "x")
+    (experts, n), kw = _mx4_operand(wc, ws, 2, "w")
+    if kw != k:
+        raise ValueError("x has k = %d, w has %d" % (k, kw))
+    _shape(offsets, (experts + 1,), "offsets")
+    y = _output(y, (rows, n), dtype, xc, "y")
+    py, dt = _typed(y, "y", _HALF_TYPES)
+    pw = _workspace(workspace, "exl3_mx4_matmul_experts")
+    device = _same_device(xc, xs, offsets, wc, ws, y, workspace)
+    _call("exl3_mx4_matmul_experts", device, stream,
+          (_dev(xc, torch.uint8, "x codes"), _dev(xs, torch.uint8, "x scales"), _dev(offsets, torch.int32, "offsets"),
+           _dev(wc, torch.uint8, "w codes"), _dev(ws, torch.uint8, "w scales"), py, dt, rows, k, n, experts, pw,
+           workspace.numel()))
+    return y
+
+
+def exl3_moe_sort_workspace_size(tokens, topk, experts):
+    return int(load().exl3_moe_sort_workspace_size(tokens, topk, experts))
+
+
+def exl3_moe_sort(ids, experts, offsets=None, positions=None, workspace=None, stream=None):
+    """Order of tokens by expert for ids int32 [tokens, topk]: returns offsets
+    int32 [experts + 1] and positions int32 [tokens, topk] (-1: no row)."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be tokens x topk")
+    tokens, topk = ids.shape
+    offsets = _output(offsets, (experts + 1,), torch.int32, ids, "offsets")
+    positions = _output(positions, (tokens, topk), torch.int32, ids, "positions")
+    pw = _workspace(workspace, "exl3_moe_sort")
+    device = _same_device(ids, offsets, positions, workspace)
+    _call("exl3_moe_sort", device, stream,
+          (_dev(ids, torch.int32, "ids"), tokens, topk, experts, _dev(offsets, torch.int32, "offsets"),
+           _dev(positions, torch.int32, "positions"), pw, workspace.numel()))
+    return offsets, positions
+
+
+def _positions(positions, tokens):
+    if positions.dim() != 2 or (tokens is not None and positions.shape[0] != tokens):
+        raise ValueError("positions must be tokens x topk")
+    return _dev(positions, torch.int32, "positions"), positions.shape[1]
+
+
+def exl3_moe_gather(x, positions, out=None, out_rows=None, stream=None):
+    """out[positions[t, j]] = x[t]; `out` (or `out_rows`, default one row per
+    choice, for a new one whose other rows are not written)."""
+    if x.dim() != 2:
+        raise ValueError("x must be tokens x h")
+    tokens, h = x.shape
+    pp, topk = _positions(positions, tokens)
+    px, dt = _typed(x, "x")
+    if out is None:
+        out = torch.empty((tokens * topk if out_rows is None else int(out_rows), h), dtype=x.dtype, device=x.device)
+    elif out.dim() != 2 or out.shape[1] != h:
+        raise ValueError("out must be rows x h")
+    device = _same_device(x, positions, out)
+    _call("exl3_moe_gather", device, stream, (px, dt, pp, tokens, topk, h, out.shape[0], _dev(out, x.dtype, "out")))
+    return out
+
+
+def exl3_moe_combine(ys, positions, weights=None, y=None, stream=None):
+    """y[t] = sum over j of weights[t, j] ys[positions[t, j]] (weights fp32, None: ones)."""
+    if ys.dim() != 2:
+        raise ValueError("ys must be rows x h")
+    rows, h = ys.shape
+    pp, topk = _positions(positions, None)
+    tokens = positions.shape[0]
+    py, dt = _typed(ys, "ys")
+    if weights is not None:
+        _shape(weights, (tokens, topk), "weights")
+    y = _output(y, (tokens, h), ys.dtype, ys, "y")
+    device = _same_device(ys, positions, weights, y)
+    _call("exl3_moe_combine", device, stream,
+          (py, dt, pp, _ptr_or_none(weights, torch.float32, "weights"), tokens, topk, h, rows, _dev(y, ys.dtype, "y")))
+    return y
+
+
+def exl3_moe_combine_grad(dy, ys, positions, weights=None, dys=None, dweights=None, stream=None):
+    """Gradients of exl3_moe_combine: (dys, dweights).  Rows of dys that no
+    position names are not written."""
+    if dy.dim() != 2 or ys.dim() != 2 or dy.shape[1] != ys.shape[1]:
+        raise ValueError("dy must be tokens x h and ys rows x h")
+    tokens, h = dy.shape
+    rows = ys.shape[0]
+    pp, topk = _positions(positions, tokens)
+    pd, dt = _typed(dy, "dy")
+    if weights is not None:
+        _shape(weights, (tokens, topk), "weights")
+    dys = _output(dys, (rows, h), dy.dtype, dy, "dys")
+    dweights = _output(dweights, (tokens, topk), torch.float32, dy, "dweights")
+    device = _same_device(dy, ys, positions, weights, dys, dweights)
+    _call("exl3_moe_combine_grad", device, stream,
+          (pd, _dev(ys, dy.dtype, "ys"), dt, pp, _ptr_or_none(weights, torch.float32, "weights"), tokens, topk, h, rows,
+           _dev(dys, dy.dtype, "dys"), _dev(dweights, torch.float32, "dweights")))
+    return dys, dweights
 
 
 def exl3_workspace_status(workspace, clear=False, stream=None):
