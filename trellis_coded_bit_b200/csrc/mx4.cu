@@ -175,6 +175,7 @@ template <typename T, bool ROT>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams p)
 {
     grid_dep_wait();
+    grid_dep_launch();
     const int64_t total = p.rows * p.groups;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     // rounded up to whole warps: every lane takes part in the shuffles
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *__r
                                                              int groups, int stride, T *__restrict__ w)
 {
     grid_dep_wait();
+    grid_dep_launch();
     const int64_t total = rows * groups;
     for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < total; g += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = g / groups;

@@ -41,39 +41,43 @@
 
 namespace exl3 {
 
-constexpr int kMxBM = 128;                       // output channels per tile (TMEM lanes)
+constexpr int kMxBM = 128;                       // output channels per CTA's tile (TMEM lanes)
 constexpr int kMxBK = 256;                       // columns of k per unit: 128 bytes of codes
-constexpr int kMxScaleWarp0 = 2, kMxEpiWarp0 = 6;
-constexpr int kMxThreads = 32 * (kMxEpiWarp0 + 4);
+constexpr int kMxScaleWarp0 = 2, kMxScaleWarps = 2, kMxEpiWarp0 = kMxScaleWarp0 + kMxScaleWarps;
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 16 KB
 constexpr int kMxMaxExperts = 1024;
 constexpr size_t kMxSyncArea = 64 * 1024;
+constexpr int kMxSmemLimit = 232448 - 4 * (kMxMaxExperts + 1);  // what the tile table leaves
 
-// Sizes that follow from the token tile.
-template <int TN>
+// Sizes that follow from the token tile TN and the CTAs that share it (CG).
+template <int TN, int CG>
 struct MxTile {
-    static constexpr int kBBytes = TN * kMxBK / 2;
-    static constexpr int kBGroups = (TN + 127) / 128;          // 128-row groups of token scales
+    static constexpr int kBRows = TN / CG;                      // token rows in this CTA's shared memory
+    static constexpr int kBBytes = kBRows * kMxBK / 2;
+    static constexpr int kBGroups = (TN + 127) / 128;           // 128-row groups of token scales
     static constexpr int kScaleBytes = 1024 + kBGroups * 1024;  // two 128-column chunks of 512 bytes per group
     static constexpr int kStageBytes = kMxABytes + kBBytes + kScaleBytes;
-    static constexpr int kRowsPerThread = 1 + kBGroups;         // scale rows of a scale thread
-    static constexpr int kDepth = TN > 128 ? 2 : 4;             // 512-column steps of scales in flight
-    static constexpr int kRingBytes = kDepth * kRowsPerThread * 128 * 16;
-    static constexpr int kStages = TN > 128 ? 4 : (TN > 64 ? 6 : (TN > 32 ? 7 : 8));
+    static constexpr int kARows = kMxBM / (32 * kMxScaleWarps);  // scale rows of a scale thread: weights
+    static constexpr int kXRows = (TN + 32 * kMxScaleWarps - 1) / (32 * kMxScaleWarps);  // and tokens
+    static constexpr int kDepth = TN > 64 ? 2 : 4;              // 512-column steps of scales in flight
+    static constexpr int kFit = (kMxSmemLimit - 2048) / kStageBytes;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kAcc = TN > 128 ? 1 : 2;               // accumulators in TMEM
     static constexpr int kScaleCols = 8 + 8 * kBGroups;         // TMEM columns of a stage's scales
     static constexpr int kAccCols = TN < 32 ? 32 : TN;
-    static constexpr int kSmem = 1024 + 1024 + kStages * kStageBytes + kRingBytes;
+    static constexpr int kEpiWarps = TN >= 128 ? 8 : 4;         // each: 32 lanes x kEpiCols columns
+    static constexpr int kEpiCols = TN / (kEpiWarps / 4);
+    static constexpr int kThreads = 32 * (kMxEpiWarp0 + kEpiWarps);
+    static constexpr int kSmem = 2048 + kStages * kStageBytes;
     static_assert(kAcc * kAccCols + kStages * kScaleCols <= 512, "TMEM columns");
-    static_assert(kSmem + 4 * (kMxMaxExperts + 1) <= 232448, "shared memory");
 };
 
 struct MxParams {
     const uint8_t *xs, *ws;     // scales, row-major
     const int32_t *offsets;     // [experts + 1] first token row of each expert, or null: one expert, all rows
     void *y;
-    float *partials;            // [2 G][TN][128]
-    uint32_t *counters;         // [G]
+    float *partials;            // [2 CTAs][TN / 4][128][4]
+    uint32_t *counters;         // [CTAs]
     uint32_t *status;
     int64_t rows;               // token rows
     int n, k, kb_count, experts, stride;
@@ -81,7 +85,7 @@ struct MxParams {
 };
 
 struct MxBars {
-    uint64_t tfull[8], sfull[8], empty[8];
+    uint64_t full[8], empty[8];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem_slot;
     int epi_abort;
@@ -89,38 +93,129 @@ struct MxBars {
 };
 static_assert(sizeof(MxBars) <= 1024, "barrier block");
 
+// ------------------------------------------- instructions, by CTA group ---
+
+#define EXL3_MX_MMA(cg)                                                                                          \
+    asm volatile(                                                                                                \
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"                                                              \
+        "tcgen05.mma.cta_group::" cg ".kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" \
+        ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                          \
+        : "memory")
+
+template <int CG>
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
                                          uint32_t sb, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+    if constexpr (CG == 1)
+        EXL3_MX_MMA("1");
+    else
+        EXL3_MX_MMA("2");
 }
 
 // 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, repeated in the
-// four lane quarters.
+// four lane quarters (with CG = 2 in both CTAs, each from its own shared memory).
+template <int CG>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
 {
     const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3fffu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
+// Arrives on `bar` (with CG = 2 on that of both CTAs) when the MMAs and copies
+// issued so far are done.
+template <int CG>
+__device__ __forceinline__ void mx_commit(uint64_t *bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
+    if constexpr (CG == 1)
+        mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                smem_addr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
 }
 
-// 16 bytes to shared memory, zeros if !valid (src is then not read).
-__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, bool valid)
+template <int CG>
+__device__ __forceinline__ void mx_tmem_alloc(uint32_t *slot)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
+    if constexpr (CG == 1) {
+        tmem_alloc(slot, 512);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_addr(slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void mx_tmem_dealloc(uint32_t taddr)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, 512);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;\n" ::: "memory");
+}
+
+// The barrier at `bar`'s place in the cluster's CTA 0.
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(a) : "r"(smem_addr(bar)));
+    return a;
+}
+
+// Arrives there.  What the arrival orders stays within this SM (its scales in
+// shared memory and its accumulators in TMEM, which the pair's MMAs read and
+// write on this SM), so the default scope is enough; a release at cluster scope
+// waits for every load and store in flight and cost 1200 to 2000 cycles a unit.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(leader_addr(bar)) : "memory");
+}
+
+// True in one lane of the converged warp.  The MMA issuer runs its loop with
+// the whole warp and elects the lane only around the instructions: inside an
+// `if (lane == 0)` the compiler cannot see that the operands are uniform, and
+// a unit's issue took 950 cycles instead of the tensor core's 520.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// A box of codes into this CTA's shared memory; its bytes count on `bar`, with
+// CG = 2 the leader's (a shared::cluster address).
+template <int CG>
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+                smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+            "%3}], [%4];\n" ::"r"(smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 
 #define EXL3_TMEM_LD16(taddr, v)                                                                          \
@@ -133,17 +228,17 @@ __device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, boo
                  : "r"(taddr)                                                                              \
                  : "memory")
 
-// kind::mxf4: A and B e2m1, both K-major, e8m0 scales, M = 128, N = TN; the
-// scale ids (which half of a 4-scale word) go in per MMA.
-template <int TN>
+// kind::mxf4: A and B e2m1, both K-major, e8m0 scales, M = 128 per CTA, N = TN;
+// `half` selects the scales within a word of four.
+template <int TN, int CG>
 __device__ __forceinline__ constexpr uint32_t mx_idesc(int half)
 {
     return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(kMxBM >> 4) << 24) | ((uint32_t)(2 * half) << 29);
+           ((uint32_t)((kMxBM * CG) >> 4) << 24) | ((uint32_t)(2 * half) << 29);
 }
 
 // Where a tile lies: token rows [row, row_end), the weight row and the output
-// channel of its first lane.
+// channel of the first lane (of CTA 0 where two share the tile).
 struct MxPlace {
     int64_t wrow;
     int64_t row, row_end;
@@ -164,7 +259,7 @@ __device__ __forceinline__ void mx_expert_rows(const MxParams &p, int e, int64_t
 
 // Tile t: its expert from the tiles' prefix sums (smem), then token tiles
 // fastest within a row of channels, so that neighbouring tiles share weights.
-template <int TN>
+template <int TN, int CG>
 __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const uint32_t *first, uint32_t t)
 {
     int lo = 0, hi = p.experts;  // first[lo] <= t < first[hi]
@@ -182,59 +277,355 @@ __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const uint32_t *f
     const uint32_t tts = (uint32_t)((w.row_end - r0 + TN - 1) / TN);
     const uint32_t nt = local / tts;
     w.row = r0 + (int64_t)(local - nt * tts) * TN;
-    w.ch = (int)nt * kMxBM;
+    w.ch = (int)nt * (kMxBM * CG);
     w.wrow = (int64_t)lo * p.n + w.ch;
     return w;
 }
 
-__device__ __forceinline__ uint32_t mx_begin(uint64_t c, uint64_t U, uint64_t G)
+// ------------------------------------------------------------ schedule ---
+//
+// T tiles on G workers (a CTA, or the pair of CTAs that shares a tile).  The
+// last T mod G tiles are split: their units (tile, 256 columns) in order, an
+// equal share for each worker, done first so that the sums meet while the
+// whole tiles run.  Then worker c takes the whole tiles c, c + G, ...:
+// at any time the workers are on neighbouring tiles, which share weights, so
+// that these come from memory once.  (With contiguous shares instead, 74 pairs
+// held 74 different rows of weights: 2048 x 8192 x 18944 took 241 us, waiting
+// 3.4 us for each copy.)
+struct MxSched {
+    uint32_t worker, G, KB;
+    uint32_t whole;      // whole tiles of each worker
+    uint32_t split0;     // first split tile
+    uint32_t U, W;       // units of the split tiles, workers that share them
+    uint32_t u0, u1;     // this worker's
+    int split_segs, segs;
+};
+
+// Part [k0, k1) of tile t.
+struct MxSeg {
+    uint32_t t;
+    int k0, k1;
+};
+
+__device__ __forceinline__ uint32_t mx_begin(const MxSched &m, uint32_t c)
 {
-    return (uint32_t)(c * U / G);
+    return (uint32_t)((uint64_t)c * m.U / m.W);
 }
 
-// The CTA that owns unit u.
-__device__ __forceinline__ uint32_t mx_owner(uint64_t u, uint64_t U, uint64_t G)
+// The worker that owns unit u of the split tiles.
+__device__ __forceinline__ uint32_t mx_owner(const MxSched &m, uint32_t u)
 {
-    return (uint32_t)(((u + 1) * G - 1) / U);
+    return (uint32_t)((((uint64_t)u + 1) * m.W - 1) / m.U);
 }
 
-// Partial slot of CTA c's segment of the tile that begins at unit tb: its
-// first segment uses 2c, its last 2c + 1.
-__device__ __forceinline__ uint32_t mx_slot(uint32_t c, uint32_t tb, uint64_t U, uint64_t G)
+// Partial slot of worker c's segment of the split tile that begins at unit tb:
+// its first segment uses 2c, its second 2c + 1.
+__device__ __forceinline__ uint32_t mx_slot(const MxSched &m, uint32_t c, uint32_t tb)
 {
-    return mx_begin(c, U, G) >= tb ? 2 * c : 2 * c + 1;
+    return mx_begin(m, c) >= tb ? 2 * c : 2 * c + 1;
 }
 
+__device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint32_t workers, uint32_t worker)
+{
+    MxSched m;
+    m.worker = worker;
+    m.G = workers;
+    m.KB = KB;
+    m.whole = tiles / workers;
+    m.split0 = m.whole * workers;
+    m.U = (tiles - m.split0) * KB;
+    // no more workers than units: with an empty share between two others a
+    // tile's segments would be miscounted
+    m.W = m.U < workers ? m.U : workers;
+    m.u0 = m.u1 = 0;
+    m.split_segs = 0;
+    if (worker < m.W) {
+        m.u0 = mx_begin(m, worker);
+        m.u1 = mx_begin(m, worker + 1);
+        m.split_segs = (int)((m.u1 - 1) / KB - m.u0 / KB) + 1;
+    }
+    m.segs = m.split_segs + (int)m.whole;
+    return m;
+}
+
+__device__ __forceinline__ MxSeg mx_seg(const MxSched &m, int i)
+{
+    MxSeg g;
+    if (i >= m.split_segs) {
+        g.t = m.worker + (uint32_t)(i - m.split_segs) * m.G;
+        g.k0 = 0;
+        g.k1 = (int)m.KB;
+    } else {
+        const uint32_t tile = m.u0 / m.KB + (uint32_t)i, b = tile * m.KB;
+        g.t = m.split0 + tile;
+        g.k0 = b < m.u0 ? (int)(m.u0 - b) : 0;
+        g.k1 = b + m.KB < m.u1 ? (int)m.KB : (int)(m.u1 - b);
+    }
+    return g;
+}
+
+// ------------------------------------------------------------ epilogue ---
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    T v[2] = {from_f32<T>(a), from_f32<T>(b)};
+    uint32_t r;
+    memcpy(&r, v, 4);
+    return r;
+}
+
+// Stores 8 tokens x 32 channels: v[i] holds the lane's channel of tokens 2i and
+// 2i + 1.  Three butterfly exchanges (lanes 1, 2, 4 apart) turn 8 tokens of one
+// channel into 8 channels of one token, so that 4 lanes store the 64 contiguous
+// bytes of a token's 32 channels (`wide`: y's rows are 16-byte aligned).
+// Otherwise each lane stores its own channel 8 times.  yt: y at the first token
+// and the warp's first channel; ch_left: channels of y from there on.
+template <typename T>
+__device__ __forceinline__ void mx_store8(T *yt, int64_t n, const uint32_t *v, int tokens, int ch_left, bool wide)
+{
+    const int lane = threadIdx.x & 31;
+    if (wide) {
+        // lanes 1 apart: register i becomes (channel pair, token 2i + (lane & 1))
+        const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+        uint32_t a[4], c[4], e[4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            // the halves the neighbour needs, of two registers at once
+            const uint32_t give = __byte_perm(v[i], v[i + 1], b0 ? 0x5410 : 0x7632);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+            a[i] = b0 ? __byte_perm(got, v[i], 0x7610) : __byte_perm(v[i], got, 0x5410);
+            a[i + 1] = b0 ? __byte_perm(got, v[i + 1], 0x7632) : __byte_perm(v[i + 1], got, 0x7610);
+        }
+        // lanes 2 apart: register pairs (0, 1) and (2, 3); afterwards c[2h], c[2h + 1]
+        // are 4 channels of token 4h + 2 (b1) + b0
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? a[2 * h] : a[2 * h + 1], 2);
+            c[2 * h] = b1 ? got : a[2 * h];
+            c[2 * h + 1] = b1 ? a[2 * h + 1] : got;
+        }
+        // lanes 4 apart: 8 channels of token 4 (b2) + 2 (b1) + b0
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b2 ? c[h] : c[2 + h], 4);
+            e[h] = b2 ? got : c[h];
+            e[2 + h] = b2 ? c[2 + h] : got;
+        }
+        const int token = lane & 7, group = lane & 24;
+        if (token < tokens && group < ch_left)
+            *reinterpret_cast<uint4 *>(yt + token * n + group) = make_uint4(e[0], e[1], e[2], e[3]);
+    } else if (lane < ch_left) {
+        uint16_t *q = reinterpret_cast<uint16_t *>(yt + lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < tokens)
+                q[i * n] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+template <int TN, int CG>
 __device__ __forceinline__ void mx_epi_sync()
 {
-    asm volatile("bar.sync 1, 128;\n" ::: "memory");
+    asm volatile("bar.sync 1, %0;\n" ::"n"(32 * MxTile<TN, CG>::kEpiWarps) : "memory");
 }
 
-template <typename T, int TN>
-__global__ void __launch_bounds__(kMxThreads, 1)
+// Segment `seg` of this worker.  Returns false if its accumulators never came
+// (the caller stops).
+template <typename T, int TN, int CG>
+__device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, const uint32_t *first, const MxSched &sched,
+                                            uint32_t tmem, int seg, uint32_t rank)
+{
+    using S = MxTile<TN, CG>;
+    constexpr int kCols = S::kEpiCols;
+    volatile int *epi_abort = &bars.epi_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quarter = warp & 3;                                  // TMEM lanes this warp may access
+    const int c0 = (warp - kMxEpiWarp0) / 4 * kCols;               // its columns
+    const MxSeg g = mx_seg(sched, seg);
+    const bool whole = g.k0 == 0 && g.k1 == (int)sched.KB;
+    const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+    const int acc = seg % S::kAcc;
+    const uint32_t par = (uint32_t)(seg / S::kAcc) & 1u;
+    bool ok = true;
+    if (lane == 0) {
+        const uint64_t t0 = global_ns();
+        while (!mbar_try_wait(&bars.acc_full[acc], par)) {
+            __nanosleep(100);
+            if (global_ns() - t0 > p.wait_ns) {
+                ok = false;
+                break;
+            }
+        }
+        if (!ok) {
+            record_timeout(p.status);
+            *epi_abort = 1;
+        }
+    }
+    // the epilogue warps agree, so that none is left at a barrier of the
+    // others (only they write the flag, and only before this barrier)
+    mx_epi_sync<TN, CG>();
+    const bool stop = *epi_abort != 0;
+    mx_epi_sync<TN, CG>();
+    if (stop)
+        return false;
+    mbar_wait(&bars.acc_full[acc], par, kDefaultWaitNs);  // complete: every lane observes it
+    tc_fence_after();
+
+    const uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * S::kAccCols + c0);
+    const int64_t cols64 = w.row_end - w.row - c0;
+    const int cols = cols64 < kCols ? (int)cols64 : kCols;         // this warp's tokens (may be <= 0)
+    const int ch = w.ch + (int)rank * kMxBM + quarter * 32;        // the warp's first channel
+    const int ch_left = p.n - ch;
+    const bool wide = (p.n & 7) == 0;
+    T *const y = reinterpret_cast<T *>(p.y) + (w.row + c0) * p.n + ch;
+
+    if (whole) {
+        // everything into registers (16 bits each), so that the MMA issuer
+        // gets the accumulator back before the stores
+        uint32_t v[kCols / 2];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+            uint32_t b[16];
+            EXL3_TMEM_LD16(d + c, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[c / 2 + i] = pack2<T>(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (CG == 1)
+                mbar_arrive(&bars.acc_empty[acc]);
+            else
+                mbar_arrive_leader(&bars.acc_empty[acc]);
+        }
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8)
+            if (c < cols)
+                mx_store8<T>(y + (int64_t)c * p.n, p.n, v + c / 2, cols - c, ch_left, wide);
+        return true;
+    }
+
+    // A split tile: fp32 partials to the workspace, [4 columns][lane][4]
+    const uint32_t tb = (g.t - sched.split0) * sched.KB;
+    const uint32_t c_lo = mx_owner(sched, tb);
+    const int nseg = (int)(mx_owner(sched, tb + sched.KB - 1) - c_lo) + 1;
+    constexpr size_t kSlot = (size_t)TN * kMxBM;
+    const size_t lane_at = (size_t)(c0 / 4) * (4 * kMxBM) + (size_t)(quarter * 32 + lane) * 4;
+    float *const mine = p.partials + ((size_t)mx_slot(sched, sched.worker, tb) * CG + rank) * kSlot + lane_at;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+        uint32_t b[16];
+        EXL3_TMEM_LD16(d + c, b);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (c + 4 * g < cols)
+                __stcg(reinterpret_cast<float4 *>(mine + (size_t)(c / 4 + g) * (4 * kMxBM)),
+                       make_float4(__uint_as_float(b[4 * g]), __uint_as_float(b[4 * g + 1]),
+                                   __uint_as_float(b[4 * g + 2]), __uint_as_float(b[4 * g + 3])));
+    }
+    __threadfence();
+    mx_epi_sync<TN, CG>();
+    if (threadIdx.x == 32 * kMxEpiWarp0) {
+        uint32_t *counter = &p.counters[c_lo * CG + rank];
+        const int last = atomicAdd(counter, 1u) == (uint32_t)(nseg - 1);
+        if (last)
+            *counter = 0u;  // every segment has arrived: re-arm for the next call
+        bars.ticket = last;
+        __threadfence();
+    }
+    mx_epi_sync<TN, CG>();
+    if (bars.ticket) {
+        // sums in segment order, this CTA's own from TMEM; kAhead segments'
+        // loads of 16 columns in flight
+        constexpr int kAhead = TN >= 128 ? 2 : 4;
+        const int own = (int)(sched.worker - c_lo);
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+            uint32_t b[16];
+            EXL3_TMEM_LD16(d + c, b);
+            float s[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] = 0.f;
+#pragma unroll 1
+            for (int j0 = 0; j0 < nseg; j0 += kAhead) {
+                float4 q[kAhead][4];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (j0 + j < nseg && j0 + j != own) {
+                        const float *src = p.partials +
+                                           ((size_t)mx_slot(sched, c_lo + j0 + j, tb) * CG + rank) * kSlot + lane_at +
+                                           (size_t)(c / 4) * (4 * kMxBM);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            if (c + 4 * g < cols)
+                                q[j][g] = __ldcg(reinterpret_cast<const float4 *>(src + (size_t)g * (4 * kMxBM)));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (j0 + j < nseg) {
+                        const bool o = j0 + j == own;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            s[4 * g] += o ? __uint_as_float(b[4 * g]) : q[j][g].x;
+                            s[4 * g + 1] += o ? __uint_as_float(b[4 * g + 1]) : q[j][g].y;
+                            s[4 * g + 2] += o ? __uint_as_float(b[4 * g + 2]) : q[j][g].z;
+                            s[4 * g + 3] += o ? __uint_as_float(b[4 * g + 3]) : q[j][g].w;
+                        }
+                    }
+                }
+            }
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = pack2<T>(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+            for (int h = 0; h < 16; h += 8)
+                if (c + h < cols)
+                    mx_store8<T>(y + (int64_t)(c + h) * p.n, p.n, v + h / 2, cols - c - h, ch_left, wide);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        if constexpr (CG == 1)
+            mbar_arrive(&bars.acc_empty[acc]);
+        else
+            mbar_arrive_leader(&bars.acc_empty[acc]);
+    }
+    return true;
+}
+
+// --------------------------------------------------------- main kernel ---
+
+template <typename T, int TN, int CG>
+__global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     mx4_gemm_kernel(const MxParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
-    using S = MxTile<TN>;
+    using S = MxTile<TN, CG>;
+    constexpr int ST = S::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     MxBars &bars = *reinterpret_cast<MxBars *>(smem);
     unsigned char *aring = smem + 1024;
-    unsigned char *bring = aring + S::kStages * kMxABytes;
-    unsigned char *scales = bring + S::kStages * S::kBBytes;
-    unsigned char *sring = scales + S::kStages * S::kScaleBytes;
-    uint32_t *first = reinterpret_cast<uint32_t *>(sring + S::kRingBytes);  // [experts + 1]
-    volatile int *epi_abort = &bars.epi_abort;
+    unsigned char *bring = aring + ST * kMxABytes;
+    unsigned char *scales = bring + ST * S::kBBytes;
+    uint32_t *first = reinterpret_cast<uint32_t *>(scales + ST * S::kScaleBytes);  // [experts + 1]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 1 ? 0u : cluster_rank();
+    const uint32_t worker = blockIdx.x / CG;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(&bars.tfull[s], 1);
-            mbar_init(&bars.sfull[s], 4);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&bars.full[s], 1 + CG * kMxScaleWarps);  // the bytes, each CTA's scales
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars.acc_full[b], 1);
-            mbar_init(&bars.acc_empty[b], 4);
+            mbar_init(&bars.acc_empty[b], S::kEpiWarps * CG);
         }
         mbar_init(&bars.drain, 1);
         bars.epi_abort = 0;
@@ -242,11 +633,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1)
-        tmem_alloc(&bars.tmem_slot, 512);
+        mx_tmem_alloc<CG>(&bars.tmem_slot);
     grid_dep_wait();
+    grid_dep_launch();
     if (warp == 0) {
         // prefix sums of the experts' tiles
-        const uint32_t nts = (uint32_t)((p.n + kMxBM - 1) / kMxBM);
+        const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
         uint32_t run = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             uint32_t v = 0;
@@ -270,294 +662,241 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem = bars.tmem_slot;
-    const uint32_t KB = (uint32_t)p.kb_count;
-    const uint64_t U = (uint64_t)first[p.experts] * KB;
-    // no more CTAs than units: with an empty range between two others a
-    // tile's segments would be miscounted
-    const uint64_t G = U < gridDim.x ? U : gridDim.x;
-    const bool works = blockIdx.x < G;
-    const uint32_t u0 = works ? mx_begin(blockIdx.x, U, G) : 0, u1 = works ? mx_begin(blockIdx.x + 1, U, G) : 0;
-    const int nu = (int)(u1 - u0);
+    const int KB = p.kb_count;
+    const MxSched sched = mx_schedule(first[p.experts], (uint32_t)KB, gridDim.x / CG, worker);
 
     if (warp == 0) {
         // ---------------------------------------------------- producer ---
-        if (lane == 0 && nu > 0) {
-            uint32_t t = u0 / KB;
-            int kb = (int)(u0 - t * KB);
-            MxPlace w = mx_place<TN>(p, first, t);
-            int issued = 0;
-            for (int i = 0; i < nu; ++i) {
-                const int s = i % S::kStages;
-                if (!mbar_wait(&bars.empty[s], ((uint32_t)(i / S::kStages) & 1u) ^ 1u, p.wait_ns)) {
-                    record_timeout(p.status);
-                    break;
-                }
-                mbar_arrive_expect_tx(&bars.tfull[s], kMxABytes + S::kBBytes);
-                tma_load_2d(aring + s * kMxABytes, &wmap, kb * (kMxBK / 2), (int)w.wrow, &bars.tfull[s]);
-                tma_load_2d(bring + s * S::kBBytes, &xmap, kb * (kMxBK / 2), (int)w.row, &bars.tfull[s]);
-                issued = i + 1;
-                if (++kb == (int)KB && i + 1 < nu) {
-                    kb = 0;
-                    w = mx_place<TN>(p, first, ++t);
+        // A stage's bytes, both CTAs' with CG = 2, count on the leader's barrier.
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            for (int seg = 0; seg < sched.segs && ok; ++seg) {
+                const MxSeg g = mx_seg(sched, seg);
+                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                const int wrow = (int)w.wrow + (int)rank * kMxBM, xrow = (int)w.row + (int)rank * S::kBRows;
+                for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
+                    const int s = i % ST;
+                    ok = mbar_wait(&bars.empty[s], ((uint32_t)(i / ST) & 1u) ^ 1u, p.wait_ns);
+                    if (!ok)
+                        break;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
+                    const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
+                    tma_load_2d<CG>(aring + s * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, bar);
+                    tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, kb * (kMxBK / 2), xrow, bar);
                 }
             }
-            for (int i = (issued > S::kStages ? issued - S::kStages : 0); i < issued; ++i)
-                if (!mbar_wait(&bars.tfull[i % S::kStages], (uint32_t)(i / S::kStages) & 1u, kDefaultWaitNs))
-                    record_timeout(p.status);
-        }
-    } else if (warp == 1) {
-        // -------------------------------------------------- MMA issuer ---
-        if (lane == 0 && nu > 0) {
-            int kb = (int)(u0 % KB);
-            int seg = 0;
-            bool ok = true;
-            for (int i = 0; i < nu; ++i) {
-                const bool seg_start = i == 0 || kb == 0;
-                const bool seg_end = i == nu - 1 || kb == (int)KB - 1;
-                const int acc = seg % S::kAcc;
-                if (seg_start && seg >= S::kAcc) {
-                    if (!mbar_wait(&bars.acc_empty[acc], (uint32_t)(seg / S::kAcc - 1) & 1u, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                const int s = i % S::kStages;
-                const uint32_t par = (uint32_t)(i / S::kStages) & 1u;
-                if (!mbar_wait(&bars.tfull[s], par, p.wait_ns) || !mbar_wait(&bars.sfull[s], par, p.wait_ns)) {
+            // copies in flight end before the CTA does (the second CTA of a
+            // pair leaves after the first, at the closing barrier)
+            for (int j = (i > ST ? i - ST : 0); j < i && rank == 0; ++j)
+                if (!mbar_wait(&bars.full[j % ST], (uint32_t)(j / ST) & 1u, kDefaultWaitNs)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * S::kAccCols);
-                const uint32_t tsa = tmem + (uint32_t)(S::kAcc * S::kAccCols + s * S::kScaleCols);
-                const uint32_t tsb = tsa + 8;
-                const uint32_t sc = smem_addr(scales + s * S::kScaleBytes);
-                // chunk c's scales: weights at tsa + 4c, tokens at tsb + 4 groups c
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    tmem_copy_scales(tsa + 4 * c, sc + 512 * c);
-#pragma unroll
-                    for (int g = 0; g < S::kBGroups; ++g)
-                        tmem_copy_scales(tsb + 4 * (c * S::kBGroups + g), sc + 1024 + 512 * (c * S::kBGroups + g));
-                }
-                const uint32_t a0 = smem_addr(aring + s * kMxABytes);
-                const uint32_t b0 = smem_addr(bring + s * S::kBBytes);
-                const int left = p.k - kb * kMxBK;
-                const int steps = left >= kMxBK ? 4 : (left + 63) / 64;  // 64 columns per MMA; none behind k
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < steps)
-                        mma_mxf4(d, smem_desc(a0 + 32 * j, 16, 1024), smem_desc(b0 + 32 * j, 16, 1024),
-                                 (j & 1) ? mx_idesc<TN>(1) : mx_idesc<TN>(0), tsa + 4 * (j >> 1),
-                                 tsb + 4 * S::kBGroups * (j >> 1), (!seg_start || j) ? 1u : 0u);
-                mma_commit(&bars.empty[s]);
-                if (seg_end) {
-                    mma_commit(&bars.acc_full[acc]);
-                    ++seg;
-                }
-                if (++kb == (int)KB)
-                    kb = 0;
-            }
             if (!ok)
                 record_timeout(p.status);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && sched.segs > 0) {
+            // ------------------------------------------------ MMA issuer ---
+            const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t a_base = __shfl_sync(0xffffffffu, smem_addr(aring), 0);
+            const uint32_t b_base = a_base + ST * kMxABytes, s_base = b_base + ST * S::kBBytes;
+            int s = 0;
+            uint32_t par = 0;
+            bool ok = true;
+            bool ready = mbar_try_wait(&bars.full[0], 0);
+            for (int seg = 0; seg < sched.segs && ok; ++seg) {
+                const MxSeg g = mx_seg(sched, seg);
+                const int acc = seg % S::kAcc;
+                const uint32_t d = base + (uint32_t)(acc * S::kAccCols);
+                if (seg >= S::kAcc)
+                    ok = warp_wait_uniform(&bars.acc_empty[acc], (uint32_t)(seg / S::kAcc - 1) & 1u, p.wait_ns);
+                for (int kb = g.k0; kb < g.k1 && ok; ++kb) {
+                    if (!__all_sync(0xffffffffu, ready))
+                        ok = warp_wait_uniform(&bars.full[s], par, p.wait_ns);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t tsa = base + (uint32_t)(S::kAcc * S::kAccCols + s * S::kScaleCols);
+                    const uint32_t tsb = tsa + 8;
+                    const uint32_t sc = s_base + (uint32_t)(s * S::kScaleBytes);
+                    const uint64_t adesc = smem_desc(a_base + (uint32_t)(s * kMxABytes), 16, 1024);
+                    const uint64_t bdesc = smem_desc(b_base + (uint32_t)(s * S::kBBytes), 16, 1024);
+                    const int left = p.k - kb * kMxBK;
+                    const int steps = left >= kMxBK ? 4 : (left + 63) / 64;  // 64 columns per MMA; none behind k
+                    uint64_t *const done = &bars.empty[s];
+                    if (elect_one()) {
+                        // chunk c's scales: weights at tsa + 4c, tokens at tsb + 4 groups c
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tmem_copy_scales<CG>(tsa + 4 * c, sc + 512 * c);
+#pragma unroll
+                            for (int h = 0; h < S::kBGroups; ++h)
+                                tmem_copy_scales<CG>(tsb + 4 * (c * S::kBGroups + h),
+                                                     sc + 1024 + 512 * (c * S::kBGroups + h));
+                        }
+                        // 64 columns are 32 bytes: 2 in the descriptors' address field
+                        auto mma = [&](int j, uint32_t add) {
+                            mma_mxf4<CG>(d, adesc + 2 * j, bdesc + 2 * j,
+                                         (j & 1) ? mx_idesc<TN, CG>(1) : mx_idesc<TN, CG>(0), tsa + 4 * (j >> 1),
+                                         tsb + 4 * S::kBGroups * (j >> 1), add);
+                        };
+                        mma(0, kb > g.k0 ? 1u : 0u);
+                        if (steps == 4) {
+                            mma(1, 1u);
+                            mma(2, 1u);
+                            mma(3, 1u);
+                        } else {
+                            if (steps > 1)
+                                mma(1, 1u);
+                            if (steps > 2)
+                                mma(2, 1u);
+                        }
+                        mx_commit<CG>(done);
+                        if (kb + 1 == g.k1)
+                            mx_commit<CG>(&bars.acc_full[acc]);
+                    }
+                    if (++s == ST) {
+                        s = 0;
+                        par ^= 1u;
+                    }
+                    ready = (kb + 1 < g.k1 || seg + 1 < sched.segs) && mbar_try_wait(&bars.full[s], par);
+                }
+            }
             // no MMA may still be writing TMEM when the CTA tears down
-            mma_commit(&bars.drain);
-            if (!mbar_wait(&bars.drain, 0, kDefaultWaitNs))
+            __syncwarp();
+            if (elect_one())
+                mx_commit<CG>(&bars.drain);
+            __syncwarp();
+            ok = warp_wait_uniform(&bars.drain, 0, kDefaultWaitNs) && ok;
+            if (!ok && lane == 0)
                 record_timeout(p.status);
         }
     } else if (warp < kMxEpiWarp0) {
         // ------------------------------------------------------ scales ---
-        // Thread r copies row r of the weights and rows r (and r + 128) of the
-        // tokens, 512 columns per step; a segment's steps begin at the pair
-        // that holds its first unit.
+        // Thread r owns every 64th row of the weights and of the tokens from
+        // row r on.  It loads 16 scales of each (512 columns, a step) kDepth
+        // steps ahead into registers and deals them out to the stages.
+        constexpr int NT = 32 * kMxScaleWarps;
+        constexpr int NR = S::kARows + S::kXRows;
         const int r = threadIdx.x - 32 * kMxScaleWarp0;
-        unsigned char *mine = sring + r * 16;  // [depth][row][128 threads][16 bytes]
-        const uint32_t dst_off = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
         const int kblocks = p.k / kMx4Block;
-        // issue side: (tile, pair) of the next step to copy
-        uint32_t ft = nu > 0 ? u0 / KB : 0;
-        int fkb = nu > 0 ? (int)(u0 - ft * KB) : 0;
+        // load side: segment, unit and place of the next step
+        int fseg = 0, fkb = 0, fend = 0;
         MxPlace w;
-        if (nu > 0)
-            w = mx_place<TN>(p, first, ft);
-        uint32_t fu = u0;
-        auto fetch = [&](int slot) {
-            if (fu < u1) {
-                const int64_t col = (int64_t)(fkb >> 1) * 16;
-                unsigned char *to = mine + slot * (S::kRowsPerThread * 2048);
-                const bool aok = w.ch + r < p.n;
-                cp_async16_zfill(to, aok ? p.ws + (w.wrow + r) * p.stride + col : p.ws, aok);
-#pragma unroll
-                for (int g = 0; g < S::kBGroups; ++g) {
-                    const int64_t row = w.row + r + 128 * g;
-                    const bool bok = r + 128 * g < TN && row < w.row_end;
-                    cp_async16_zfill(to + (1 + g) * 2048, bok ? p.xs + row * p.stride + col : p.xs, bok);
-                }
-                // the units this step serves: to the end of the pair, the tile or the range
-                uint32_t n2 = 2 - (uint32_t)(fkb & 1);
-                if (fkb + (int)n2 > (int)KB)
-                    n2 = KB - fkb;
-                fu += n2;
-                fkb += (int)n2;
-                if (fkb == (int)KB && fu < u1) {
-                    fkb = 0;
-                    w = mx_place<TN>(p, first, ++ft);
-                }
+        auto enter = [&]() {
+            if (fseg < sched.segs) {
+                const MxSeg g = mx_seg(sched, fseg);
+                fkb = g.k0;
+                fend = g.k1;
+                w = mx_place<TN, CG>(p, first, g.t);
             }
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
-        for (int d = 0; d < S::kDepth; ++d)
-            fetch(d);
-        int kb = nu > 0 ? (int)(u0 % KB) : 0;
-        int slot = 0;
-        uint4 cur[S::kRowsPerThread];
-        for (int i = 0; i < nu; ++i) {
-            if (i == 0 || (kb & 1) == 0) {
-                // a new step: its copy is the oldest of kDepth in flight
-                asm volatile("cp.async.wait_group %0;\n" ::"n"(S::kDepth - 1) : "memory");
+        enter();
+        auto fetch = [&](uint4 (&q)[NR]) {
+            if (fseg >= sched.segs)
+                return;
+            const int64_t col = (int64_t)(fkb >> 1) * 16;
 #pragma unroll
-                for (int q = 0; q < S::kRowsPerThread; ++q)
-                    cur[q] = *reinterpret_cast<const uint4 *>(mine + (slot * S::kRowsPerThread + q) * 2048);
-                fetch(slot);
-                slot = slot + 1 == S::kDepth ? 0 : slot + 1;
-            }
-            const int s = i % S::kStages;
-            if (!warp_wait_uniform(&bars.empty[s], ((uint32_t)(i / S::kStages) & 1u) ^ 1u, p.wait_ns)) {
-                if (lane == 0)
-                    record_timeout(p.status);
-                break;
-            }
-            unsigned char *sc = scales + s * S::kScaleBytes + dst_off;
-            const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
-            const uint32_t m0 = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
-            const uint32_t m1 = left >= 8 ? 0xffffffffu : (left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
-#pragma unroll
-            for (int q = 0; q < S::kRowsPerThread; ++q) {
-                const uint32_t w0 = (kb & 1) ? cur[q].z : cur[q].x;
-                const uint32_t w1 = (kb & 1) ? cur[q].w : cur[q].y;
-                if (q == 0) {
-                    *reinterpret_cast<uint32_t *>(sc) = w0 & m0;
-                    *reinterpret_cast<uint32_t *>(sc + 512) = w1 & m1;
+            for (int j = 0; j < NR; ++j) {
+                q[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (j < S::kARows) {
+                    const int wr = (int)rank * kMxBM + r + NT * j;
+                    if (w.ch + wr < p.n)
+                        q[j] = *reinterpret_cast<const uint4 *>(p.ws + (w.wrow + wr) * p.stride + col);
                 } else {
-                    *reinterpret_cast<uint32_t *>(sc + 1024 + 512 * (q - 1)) = w0 & m0;
-                    *reinterpret_cast<uint32_t *>(sc + 1024 + 512 * (S::kBGroups + q - 1)) = w1 & m1;
+                    const int xr = r + NT * (j - S::kARows);
+                    if (xr < TN && w.row + xr < w.row_end)
+                        q[j] = *reinterpret_cast<const uint4 *>(p.xs + (w.row + xr) * p.stride + col);
                 }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.sfull[s]);
-            if (++kb == (int)KB)
-                kb = 0;
+            fkb = (fkb | 1) + 1;  // the step serves the pair's units up to the segment's end
+            if (fkb >= fend) {
+                ++fseg;
+                enter();
+            }
+        };
+        uint4 q[S::kDepth][NR];
+#pragma unroll
+        for (int d = 0; d < S::kDepth; ++d)
+            fetch(q[d]);
+        int s = 0, seg = 0, kb = 0, end = 0;
+        if (sched.segs > 0) {
+            const MxSeg g = mx_seg(sched, 0);
+            kb = g.k0;
+            end = g.k1;
         }
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-    } else {
-        // ---------------------------------------------------- epilogue ---
-        const int quarter = warp & 3;  // TMEM lanes this warp may access
-        const int r = quarter * 32 + lane;
-        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        T *const y = reinterpret_cast<T *>(p.y);
-        uint32_t u = u0;
-        for (int seg = 0; u < u1; ++seg) {
-            const uint32_t t = u / KB;
-            const uint32_t tb = t * KB, te = tb + KB;
-            const uint32_t se = te < u1 ? te : u1;
-            const bool whole = u == tb && se == te;
-            const MxPlace w = mx_place<TN>(p, first, t);
-            const int acc = seg % S::kAcc;
-            const bool ok = warp_wait(&bars.acc_full[acc], (uint32_t)(seg / S::kAcc) & 1u, p.wait_ns, 200);
-            if (!ok && lane == 0) {
-                record_timeout(p.status);
-                *epi_abort = 1;
-            }
-            // the four warps agree, so that none is left at a barrier of the
-            // others (only they write the flag, and only before this barrier)
-            mx_epi_sync();
-            const bool stop = *epi_abort != 0;
-            mx_epi_sync();
-            if (stop)
-                break;
-            tc_fence_after();
-            const uint32_t d = tmem + lane_base + (uint32_t)(acc * S::kAccCols);
-            const int64_t cols64 = w.row_end - w.row;
-            const int cols = cols64 < TN ? (int)cols64 : TN;
-            T *const yt = y + w.row * p.n + w.ch + r;
-            const bool live = w.ch + r < p.n;
-            bool finish = true;
-            uint32_t c_lo = 0;
-            int nseg = 1;
-            if (!whole) {
-                c_lo = mx_owner(tb, U, G);
-                nseg = (int)(mx_owner(te - 1, U, G) - c_lo) + 1;
-                float *slot = p.partials + (size_t)mx_slot(blockIdx.x, tb, U, G) * (TN * kMxBM) + r;
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
-                    uint32_t v[16];
-                    EXL3_TMEM_LD16(d + c, v);
+        uint32_t par = 1;
+        bool ok = true;
+        while (seg < sched.segs && ok) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        __stcg(slot + (c + i) * kMxBM, __uint_as_float(v[i]));
-                }
-                __threadfence();
-                mx_epi_sync();
-                if (threadIdx.x == 32 * kMxEpiWarp0) {
-                    const uint32_t prev = atomicAdd(&p.counters[c_lo], 1u);
-                    const int last = prev == (uint32_t)(nseg - 1);
-                    if (last) {
-                        __threadfence();
-                        p.counters[c_lo] = 0u;  // every segment has arrived: re-arm for the next call
-                    }
-                    bars.ticket = last;
-                }
-                mx_epi_sync();
-                finish = bars.ticket != 0;
-            }
-            if (finish) {
-#pragma unroll 1
-                for (int c = 0; c < cols; c += 16) {
-                    float v[16];
-                    if (whole) {
-                        uint32_t b[16];
-                        EXL3_TMEM_LD16(d + c, b);
+            for (int d = 0; d < S::kDepth; ++d) {
+                if (seg < sched.segs && ok) {
+                    const int stop = (kb | 1) + 1 < end ? (kb | 1) + 1 : end;
+                    for (; kb < stop; ++kb) {
+                        ok = warp_wait_uniform(&bars.empty[s], par, p.wait_ns);
+                        if (!ok)
+                            break;
+                        unsigned char *sc = scales + s * S::kScaleBytes;
+                        const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
+                        const uint32_t m0 = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+                        const uint32_t m1 = left >= 8 ? 0xffffffffu : (left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] = __uint_as_float(b[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] = 0.f;
-                        for (int j = 0; j < nseg; ++j) {
-                            const float *src =
-                                p.partials + (size_t)mx_slot(c_lo + j, tb, U, G) * (TN * kMxBM) + c * kMxBM + r;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[i] += __ldcg(src + i * kMxBM);
+                        for (int j = 0; j < NR; ++j) {
+                            const bool weights = j < S::kARows;
+                            const int row = r + NT * (weights ? j : j - S::kARows);
+                            if (weights || row < TN) {
+                                unsigned char *to = sc + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+                                                    (weights ? 0 : 1024 + 512 * (row >> 7));
+                                *reinterpret_cast<uint32_t *>(to) = ((kb & 1) ? q[d][j].z : q[d][j].x) & m0;
+                                *reinterpret_cast<uint32_t *>(to + (weights ? 512 : 512 * S::kBGroups)) =
+                                    ((kb & 1) ? q[d][j].w : q[d][j].y) & m1;
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (CG == 1)
+                                mbar_arrive(&bars.full[s]);
+                            else
+                                mbar_arrive_leader(&bars.full[s]);
+                        }
+                        if (++s == ST) {
+                            s = 0;
+                            par ^= 1u;
                         }
                     }
-                    if (live) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < cols)
-                                yt[(int64_t)(c + i) * p.n] = from_f32<T>(v[i]);
+                    if (kb >= end && ++seg < sched.segs) {
+                        const MxSeg g = mx_seg(sched, seg);
+                        kb = g.k0;
+                        end = g.k1;
                     }
+                    fetch(q[d]);
                 }
             }
-            // hand the accumulator back to the MMA issuer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.acc_empty[acc]);
-            u = se;
         }
+        if (!ok && lane == 0)
+            record_timeout(p.status);
+    } else {
+        // ---------------------------------------------------- epilogue ---
+        for (int seg = 0; seg < sched.segs; ++seg)
+            if (!mx_epilogue<T, TN, CG>(p, bars, first, sched, tmem, seg, rank))
+                break;
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();  // the other CTA's commits and arrivals have landed, its MMAs are done
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        mx_tmem_dealloc<CG>(tmem);
     }
 }
 
@@ -625,30 +964,49 @@ static bool valid_mx_sizes(int64_t m, int64_t k, int64_t n, int64_t experts)
            experts <= kMxMaxExperts && experts * n <= (int64_t)1 << 30;
 }
 
-template <typename T, int TN>
-static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap, int ctas,
+template <typename T, int TN, int CG>
+static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap, int workers, bool pdl,
                              cudaStream_t s)
 {
-    auto kern = mx4_gemm_kernel<T, TN>;
-    const int smem = MxTile<TN>::kSmem + 4 * (p.experts + 1);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             MxTile<TN>::kSmem + 4 * (kMxMaxExperts + 1)) != cudaSuccess)
+    using S = MxTile<TN, CG>;
+    auto kern = mx4_gemm_kernel<T, TN, CG>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + 4 * (kMxMaxExperts + 1)) !=
+        cudaSuccess)
         return EXL3_ERR_CUDA;
-    if (launch_kernel(kern, dim3(ctas), dim3(kMxThreads), (size_t)smem, s, p, wmap, xmap) != cudaSuccess)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(workers * CG));
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = (size_t)(S::kSmem + 4 * (p.experts + 1));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if constexpr (CG == 2) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = 2;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (pdl) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    if (cudaLaunchKernelEx(&cfg, kern, p, wmap, xmap) != cudaSuccess)
         return EXL3_ERR_CUDA;
     return launch_status();
 }
 
 template <typename T>
-static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap, int ctas,
-                                  cudaStream_t s)
+static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap,
+                                  int workers, bool pdl, cudaStream_t s)
 {
     switch (tn) {
-    case 16: return launch_mx<T, 16>(p, wmap, xmap, ctas, s);
-    case 32: return launch_mx<T, 32>(p, wmap, xmap, ctas, s);
-    case 64: return launch_mx<T, 64>(p, wmap, xmap, ctas, s);
-    case 128: return launch_mx<T, 128>(p, wmap, xmap, ctas, s);
-    default: return launch_mx<T, 256>(p, wmap, xmap, ctas, s);
+    case 16: return launch_mx<T, 16, 1>(p, wmap, xmap, workers, pdl, s);
+    case 32: return launch_mx<T, 32, 1>(p, wmap, xmap, workers, pdl, s);
+    case 64: return launch_mx<T, 64, 1>(p, wmap, xmap, workers, pdl, s);
+    case 128: return launch_mx<T, 128, 1>(p, wmap, xmap, workers, pdl, s);
+    default: return launch_mx<T, 256, 2>(p, wmap, xmap, workers, pdl, s);
     }
 }
 
@@ -674,11 +1032,12 @@ static exl3_status check_mx(const uint8_t *xc, const uint8_t *xs, const uint8_t 
 
 static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *offsets, const uint8_t *wc,
                           const uint8_t *ws, void *y, int dtype, int64_t m, int64_t k, int64_t n, int64_t experts,
-                          void *workspace, cudaStream_t s)
+                          void *workspace, bool pdl, cudaStream_t s)
 {
     const int tn = mx_token_tile(mx_rows_each(m, experts));
+    const int cg = tn > 128 ? 2 : 1;  // CTAs that share a tile
     CUtensorMap wmap, xmap;
-    if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, xc, m, k / 2, tn))
+    if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, xc, m, k / 2, tn / cg))
         return EXL3_ERR_CUDA;
     MxParams p;
     p.xs = xs;
@@ -696,13 +1055,15 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     p.stride = (int)mx4_scale_stride(k);
     p.wait_ns = wait_limit_ns();
     // units fit 32 bits: at most (rows/TN + experts) tiles of each channel row
-    const int64_t tiles = ((m + tn - 1) / tn + (experts > 1 ? experts : 0)) * ((n + kMxBM - 1) / kMxBM);
+    const int64_t tiles =
+        ((m + tn - 1) / tn + (experts > 1 ? experts : 0)) * ((n + kMxBM * cg - 1) / (kMxBM * cg));
     if (tiles * p.kb_count >= (int64_t)1 << 31)
         return EXL3_ERR_UNSUPPORTED;
-    const int64_t sms = num_sms();
-    const int ctas = (int)(tiles * p.kb_count < sms ? tiles * p.kb_count : sms);
-    return dtype == EXL3_F16 ? launch_mx_tile<__half>(tn, p, wmap, xmap, ctas, s)
-                             : launch_mx_tile<__nv_bfloat16>(tn, p, wmap, xmap, ctas, s);
+    const int64_t most = num_sms() / cg;
+    const int workers = (int)(tiles * p.kb_count < most ? tiles * p.kb_count : most);
+    pdl = pdl || (launch_flags() & EXL3_LAUNCH_PDL);
+    return dtype == EXL3_F16 ? launch_mx_tile<__half>(tn, p, wmap, xmap, workers, pdl, s)
+                             : launch_mx_tile<__nv_bfloat16>(tn, p, wmap, xmap, workers, pdl, s);
 }
 
 // Workspace of exl3_mx4_linear: the matmul's, then the quantised activations.
@@ -736,7 +1097,7 @@ extern "C" exl3_status exl3_mx4_matmul(const uint8_t *xc, const uint8_t *xs, con
         return st;
     if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(m, 1))
         return EXL3_ERR_WORKSPACE;
-    return run_mx(xc, xs, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, (cudaStream_t)stream);
+    return run_mx(xc, xs, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t exl3_mx4_matmul_experts_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts)
@@ -758,7 +1119,7 @@ extern "C" exl3_status exl3_mx4_matmul_experts(const uint8_t *xc, const uint8_t 
         return EXL3_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(rows, experts))
         return EXL3_ERR_WORKSPACE;
-    return run_mx(xc, xs, offsets, wc, ws, y, dtype, rows, k, n, experts, workspace, (cudaStream_t)stream);
+    return run_mx(xc, xs, offsets, wc, ws, y, dtype, rows, k, n, experts, workspace, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t exl3_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n)
@@ -790,5 +1151,6 @@ extern "C" exl3_status exl3_mx4_linear(const void *x, int dtype, const void *sig
     const exl3_status q = exl3_mx4_quantize(x, dtype, signs, rotate, nullptr, 1, m, xc, xs, m, k, stream);
     if (q != EXL3_OK)
         return q;
-    return run_mx(xc, xs, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, (cudaStream_t)stream);
+    // launched while the quantiser runs: all but the weights waits for its end
+    return run_mx(xc, xs, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, true, (cudaStream_t)stream);
 }
