@@ -43,7 +43,7 @@ namespace exl3 {
 
 constexpr int kMxBM = 128;                       // output channels per CTA's tile (TMEM lanes)
 constexpr int kMxBK = 256;                       // columns of k per unit: 128 bytes of codes
-constexpr int kMxScaleWarp0 = 2, kMxScaleWarps = 2, kMxEpiWarp0 = kMxScaleWarp0 + kMxScaleWarps;
+constexpr int kMxMmaWarp = 0, kMxFeedWarp0 = 1;  // then 1 + groups of 128 tokens feeding warps, then the epilogue
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 16 KB
 constexpr int kMxMaxExperts = 1024;
 constexpr size_t kMxSyncArea = 64 * 1024;
@@ -57,9 +57,9 @@ struct MxTile {
     static constexpr int kBGroups = (TN + 127) / 128;           // 128-row groups of token scales
     static constexpr int kScaleBytes = 1024 + kBGroups * 1024;  // two 128-column chunks of 512 bytes per group
     static constexpr int kStageBytes = kMxABytes + kBBytes + kScaleBytes;
-    static constexpr int kARows = kMxBM / (32 * kMxScaleWarps);  // scale rows of a scale thread: weights
-    static constexpr int kXRows = (TN + 32 * kMxScaleWarps - 1) / (32 * kMxScaleWarps);  // and tokens
-    static constexpr int kDepth = TN > 64 ? 2 : 4;              // 512-column steps of scales in flight
+    static constexpr int kFeedWarps = 1 + kBGroups;             // one per 128 rows of scales
+    static constexpr int kEpiWarp0 = kMxFeedWarp0 + kFeedWarps;
+    static constexpr int kDepth = 4;                            // 512-column steps of scales in flight
     static constexpr int kFit = (kMxSmemLimit - 2048) / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kAcc = TN > 128 ? 1 : 2;               // accumulators in TMEM
@@ -67,7 +67,7 @@ struct MxTile {
     static constexpr int kAccCols = TN < 32 ? 32 : TN;
     static constexpr int kEpiWarps = TN >= 128 ? 8 : 4;         // each: 32 lanes x kEpiCols columns
     static constexpr int kEpiCols = TN / (kEpiWarps / 4);
-    static constexpr int kThreads = 32 * (kMxEpiWarp0 + kEpiWarps);
+    static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
     static constexpr int kSmem = 2048 + kStages * kStageBytes;
     static_assert(kAcc * kAccCols + kStages * kScaleCols <= 512, "TMEM columns");
 };
@@ -441,7 +441,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     volatile int *epi_abort = &bars.epi_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3;                                  // TMEM lanes this warp may access
-    const int c0 = (warp - kMxEpiWarp0) / 4 * kCols;               // its columns
+    const int c0 = (warp - S::kEpiWarp0) / 4 * kCols;              // its columns
     const MxSeg g = mx_seg(sched, seg);
     const bool whole = g.k0 == 0 && g.k1 == (int)sched.KB;
     const MxPlace w = mx_place<TN, CG>(p, first, g.t);
@@ -527,7 +527,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     }
     __threadfence();
     mx_epi_sync<TN, CG>();
-    if (threadIdx.x == 32 * kMxEpiWarp0) {
+    if (threadIdx.x == 32 * S::kEpiWarp0) {
         uint32_t *counter = &p.counters[c_lo * CG + rank];
         const int last = atomicAdd(counter, 1u) == (uint32_t)(nseg - 1);
         if (last)
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     const uint32_t worker = blockIdx.x / CG;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&bars.full[s], 1 + CG * kMxScaleWarps);  // the bytes, each CTA's scales
+            mbar_init(&bars.full[s], 1 + CG * S::kFeedWarps);  // the bytes, each CTA's scales
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         bars.ticket = 0;
         fence_mbar_init();
     }
-    if (warp == 1)
+    if (warp == kMxMmaWarp)
         mx_tmem_alloc<CG>(&bars.tmem_slot);
     grid_dep_wait();
     grid_dep_launch();
@@ -669,39 +669,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     const int KB = p.kb_count;
     const MxSched sched = mx_schedule(first[p.experts], (uint32_t)KB, gridDim.x / CG, worker);
 
-    if (warp == 0) {
-        // ---------------------------------------------------- producer ---
-        // A stage's bytes, both CTAs' with CG = 2, count on the leader's barrier.
-        if (lane == 0) {
-            int i = 0;
-            bool ok = true;
-            for (int seg = 0; seg < sched.segs && ok; ++seg) {
-                const MxSeg g = mx_seg(sched, seg);
-                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
-                const int wrow = (int)w.wrow + (int)rank * kMxBM, xrow = (int)w.row + (int)rank * S::kBRows;
-                for (int kb = g.k0; kb < g.k1; ++kb, ++i) {
-                    const int s = i % ST;
-                    ok = mbar_wait(&bars.empty[s], ((uint32_t)(i / ST) & 1u) ^ 1u, p.wait_ns);
-                    if (!ok)
-                        break;
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
-                    const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
-                    tma_load_2d<CG>(aring + s * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, bar);
-                    tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, kb * (kMxBK / 2), xrow, bar);
-                }
-            }
-            // copies in flight end before the CTA does (the second CTA of a
-            // pair leaves after the first, at the closing barrier)
-            for (int j = (i > ST ? i - ST : 0); j < i && rank == 0; ++j)
-                if (!mbar_wait(&bars.full[j % ST], (uint32_t)(j / ST) & 1u, kDefaultWaitNs)) {
-                    ok = false;
-                    break;
-                }
-            if (!ok)
-                record_timeout(p.status);
-        }
-    } else if (warp == 1) {
+    if (warp == kMxMmaWarp) {
         if (rank == 0 && sched.segs > 0) {
             // ------------------------------------------------ MMA issuer ---
             const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
@@ -778,61 +746,69 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             if (!ok && lane == 0)
                 record_timeout(p.status);
         }
-    } else if (warp < kMxEpiWarp0) {
-        // ------------------------------------------------------ scales ---
-        // Thread r owns every 64th row of the weights and of the tokens from
-        // row r on.  It loads 16 scales of each (512 columns, a step) kDepth
-        // steps ahead into registers and deals them out to the stages.
-        constexpr int NT = 32 * kMxScaleWarps;
-        constexpr int NR = S::kARows + S::kXRows;
-        const int r = threadIdx.x - 32 * kMxScaleWarp0;
+    } else if (warp < S::kEpiWarp0) {
+        // ----------------------------------------------------- feeding ---
+        // Warp 0 of these issues the copies of the codes (both CTAs' bytes of
+        // a stage count on the leader's barrier) and deals out the scales of
+        // the 128 weight rows, the others those of 128 token rows each.  Lane
+        // l owns rows l, l + 32, l + 64, l + 96, whose scales of 128 columns
+        // are the 16 bytes at 16 l of the layout that the tensor core wants:
+        // one conflict-free store.  It loads 16 scales of each row (512
+        // columns, a step) kDepth steps ahead into registers.
+        const int group = warp - kMxFeedWarp0 - 1;  // -1: weights
         const int kblocks = p.k / kMx4Block;
-        // load side: segment, unit and place of the next step
+        // load side: segment, unit and rows of the next step
         int fseg = 0, fkb = 0, fend = 0;
-        MxPlace w;
+        const uint8_t *from = nullptr;  // scales of row `lane`
+        int have = 0;                   // rows from there on that exist
         auto enter = [&]() {
             if (fseg < sched.segs) {
                 const MxSeg g = mx_seg(sched, fseg);
+                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
                 fkb = g.k0;
                 fend = g.k1;
-                w = mx_place<TN, CG>(p, first, g.t);
+                const int ch = (int)rank * kMxBM + lane;
+                const int64_t left = group < 0 ? (int64_t)(p.n - w.ch - ch) : w.row_end - w.row - 128 * group - lane;
+                have = left < 0 ? 0 : (left < 128 ? (int)left : 128);
+                from = group < 0 ? p.ws + (w.wrow + ch) * p.stride : p.xs + (w.row + 128 * group + lane) * p.stride;
             }
         };
         enter();
-        auto fetch = [&](uint4 (&q)[NR]) {
+        const int most = group < 0 ? kMxBM : TN - 128 * group;  // rows of the tile
+        auto fetch = [&](uint4 (&q)[4]) {
             if (fseg >= sched.segs)
                 return;
-            const int64_t col = (int64_t)(fkb >> 1) * 16;
+            const uint8_t *src = from + (int64_t)(fkb >> 1) * 16;
 #pragma unroll
-            for (int j = 0; j < NR; ++j) {
-                q[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (j < S::kARows) {
-                    const int wr = (int)rank * kMxBM + r + NT * j;
-                    if (w.ch + wr < p.n)
-                        q[j] = *reinterpret_cast<const uint4 *>(p.ws + (w.wrow + wr) * p.stride + col);
-                } else {
-                    const int xr = r + NT * (j - S::kARows);
-                    if (xr < TN && w.row + xr < w.row_end)
-                        q[j] = *reinterpret_cast<const uint4 *>(p.xs + (w.row + xr) * p.stride + col);
-                }
-            }
+            for (int j = 0; j < 4; ++j)
+                q[j] = 32 * j < have && 32 * j + lane < most ? *reinterpret_cast<const uint4 *>(src + (int64_t)(32 * j) * p.stride)
+                                                             : make_uint4(0u, 0u, 0u, 0u);
             fkb = (fkb | 1) + 1;  // the step serves the pair's units up to the segment's end
             if (fkb >= fend) {
                 ++fseg;
                 enter();
             }
         };
-        uint4 q[S::kDepth][NR];
+        uint4 q[S::kDepth][4];
 #pragma unroll
         for (int d = 0; d < S::kDepth; ++d)
             fetch(q[d]);
-        int s = 0, seg = 0, kb = 0, end = 0;
-        if (sched.segs > 0) {
-            const MxSeg g = mx_seg(sched, 0);
-            kb = g.k0;
-            end = g.k1;
-        }
+        int s = 0, seg = 0, kb = 0, end = 0, wrow = 0, xrow = 0;
+        auto next = [&]() {
+            if (seg < sched.segs) {
+                const MxSeg g = mx_seg(sched, seg);
+                kb = g.k0;
+                end = g.k1;
+                if (group < 0) {
+                    const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                    wrow = (int)w.wrow + (int)rank * kMxBM;
+                    xrow = (int)w.row + (int)rank * S::kBRows;
+                }
+            }
+        };
+        next();
         uint32_t par = 1;
+        uint32_t issued = 0;  // stages that were ever filled: bits
         bool ok = true;
         while (seg < sched.segs && ok) {
 #pragma unroll
@@ -843,22 +819,26 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                         ok = warp_wait_uniform(&bars.empty[s], par, p.wait_ns);
                         if (!ok)
                             break;
-                        unsigned char *sc = scales + s * S::kScaleBytes;
+                        if (group < 0 && lane == 0) {
+                            if (rank == 0)
+                                mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
+                            const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
+                            tma_load_2d<CG>(aring + s * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, bar);
+                            tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, kb * (kMxBK / 2), xrow, bar);
+                        }
+                        issued |= 1u << s;
+                        unsigned char *sc = scales + s * S::kScaleBytes + lane * 16 + (group < 0 ? 0 : 1024 + 512 * group);
                         const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
                         const uint32_t m0 = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
                         const uint32_t m1 = left >= 8 ? 0xffffffffu : (left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
-#pragma unroll
-                        for (int j = 0; j < NR; ++j) {
-                            const bool weights = j < S::kARows;
-                            const int row = r + NT * (weights ? j : j - S::kARows);
-                            if (weights || row < TN) {
-                                unsigned char *to = sc + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
-                                                    (weights ? 0 : 1024 + 512 * (row >> 7));
-                                *reinterpret_cast<uint32_t *>(to) = ((kb & 1) ? q[d][j].z : q[d][j].x) & m0;
-                                *reinterpret_cast<uint32_t *>(to + (weights ? 512 : 512 * S::kBGroups)) =
-                                    ((kb & 1) ? q[d][j].w : q[d][j].y) & m1;
-                            }
-                        }
+                        const uint4 *v = q[d];
+                        const bool odd = kb & 1;
+                        *reinterpret_cast<uint4 *>(sc) =
+                            make_uint4((odd ? v[0].z : v[0].x) & m0, (odd ? v[1].z : v[1].x) & m0,
+                                       (odd ? v[2].z : v[2].x) & m0, (odd ? v[3].z : v[3].x) & m0);
+                        *reinterpret_cast<uint4 *>(sc + (group < 0 ? 512 : 512 * S::kBGroups)) =
+                            make_uint4((odd ? v[0].w : v[0].y) & m1, (odd ? v[1].w : v[1].y) & m1,
+                                       (odd ? v[2].w : v[2].y) & m1, (odd ? v[3].w : v[3].y) & m1);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -872,14 +852,27 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                             par ^= 1u;
                         }
                     }
-                    if (kb >= end && ++seg < sched.segs) {
-                        const MxSeg g = mx_seg(sched, seg);
-                        kb = g.k0;
-                        end = g.k1;
+                    if (kb >= end) {
+                        ++seg;
+                        next();
                     }
                     fetch(q[d]);
                 }
             }
+        }
+        // copies in flight end before the CTA does (the second CTA of a pair
+        // leaves after the first, at the closing barrier).  Stages from s on
+        // were last filled in the round before this one.  If arrivals are
+        // missing, the limit that the first wait runs out of is long enough
+        // for all of them.
+        if (group < 0 && rank == 0) {
+            bool landed = true;
+            for (int j = 0; j < ST && landed; ++j) {
+                const int st = s + j < ST ? s + j : s + j - ST;
+                if (issued >> st & 1u)
+                    landed = warp_wait_uniform(&bars.full[st], st >= s ? par : par ^ 1u, kDefaultWaitNs);
+            }
+            ok = ok && landed;
         }
         if (!ok && lane == 0)
             record_timeout(p.status);
@@ -894,7 +887,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     __syncthreads();
     if constexpr (CG == 2)
         cluster_sync();  // the other CTA's commits and arrivals have landed, its MMAs are done
-    if (warp == 1) {
+    if (warp == kMxMmaWarp) {
         tc_fence_after();
         mx_tmem_dealloc<CG>(tmem);
     }
