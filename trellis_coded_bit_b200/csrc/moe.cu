@@ -13,6 +13,8 @@
 // and the gradient of gather is combine without weights.  Every sum runs in
 // fp32 in a fixed order, and no kernel uses a floating-point atomic, so
 // results are deterministic.
+#include <type_traits>
+
 #include "dtypes.cuh"
 #include "exl3_device.cuh"
 #include "exl3_host.h"
@@ -158,14 +160,27 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const int32_t *
 
 // ------------------------------------------------------ gather, combine ---
 
+// V elements (16 bytes, or one element), loaded and unpacked in two steps, so
+// that several loads can be in flight as bits.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[V])
+using Raw = typename std::conditional<V == 1, T, uint4>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *p)
+{
+    return *reinterpret_cast<const Raw<T, V> *>(p);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack_raw(const Raw<T, V> &raw, float (&v)[V])
 {
     if constexpr (V == 1)
-        v[0] = to_f32(*p);
+        v[0] = to_f32(raw);
     else
-        unpack16<T>(*reinterpret_cast<const uint4 *>(p), v);
+        unpack16<T>(raw, v);
 }
+
+constexpr int kAhead = 4;  // rows or vectors whose loads a thread keeps in flight
 
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[V])
@@ -219,16 +234,29 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const T *__restrict__ 
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 acc[i] = 0.f;
-            for (int j = 0; j < topk; ++j) {
-                const int64_t p = row_or_none(pos[j], rows);
-                if (p < 0)
-                    continue;
-                float v[V];
-                load_vec<T, V>(ys + p * h + c * V, v);
-                const float w = weights ? weights[t * topk + j] : 1.f;
+            // kAhead rows' loads in flight, added in the order of j
+            for (int j0 = 0; j0 < topk; j0 += kAhead) {
+                int64_t p[kAhead];
+                float w[kAhead];
+                Raw<T, V> raw[kAhead];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    acc[i] = fmaf(w, v[i], acc[i]);
+                for (int j = 0; j < kAhead; ++j) {
+                    p[j] = j0 + j < topk ? row_or_none(pos[j0 + j], rows) : -1;
+                    w[j] = weights && j0 + j < topk ? weights[t * topk + j0 + j] : 1.f;
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (p[j] >= 0)
+                        raw[j] = load_raw<T, V>(ys + p[j] * h + c * V);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (p[j] >= 0) {
+                        float v[V];
+                        unpack_raw<T, V>(raw[j], v);
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            acc[i] = fmaf(w[j], v[i], acc[i]);
+                    }
             }
             store_vec<T, V>(y + t * h + c * V, acc);
         }
@@ -254,20 +282,38 @@ __global__ void __launch_bounds__(256) moe_combine_grad_kernel(const T *__restri
         if (p >= 0) {
             const float w = weights ? weights[i] : 1.f;
             const T *g = dy + (i / topk) * h;
-            for (int64_t c = (int64_t)lane * V; c < h; c += 32 * V) {
-                float a[V], b[V];
-                load_vec<T, V>(g + c, a);
-                if (dweights) {
-                    load_vec<T, V>(ys + p * h + c, b);
+            const T *f = ys + p * h;
+            T *out = dys + p * h;
+            for (int64_t c0 = (int64_t)lane * V; c0 < h; c0 += 32 * V * kAhead) {
+                Raw<T, V> ra[kAhead], rb[kAhead];
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        dot = fmaf(a[e], b[e], dot);
+                for (int j = 0; j < kAhead; ++j) {
+                    const int64_t c = c0 + j * 32 * V;
+                    if (c < h) {
+                        ra[j] = load_raw<T, V>(g + c);
+                        if (dweights)
+                            rb[j] = load_raw<T, V>(f + c);
+                    }
                 }
-                if (dys) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        b[e] = w * a[e];
-                    store_vec<T, V>(dys + p * h + c, b);
+                for (int j = 0; j < kAhead; ++j) {
+                    const int64_t c = c0 + j * 32 * V;
+                    if (c < h) {
+                        float a[V], b[V];
+                        unpack_raw<T, V>(ra[j], a);
+                        if (dweights) {
+                            unpack_raw<T, V>(rb[j], b);
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                dot = fmaf(a[e], b[e], dot);
+                        }
+                        if (dys) {
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                b[e] = w * a[e];
+                            store_vec<T, V>(out + c, b);
+                        }
+                    }
                 }
             }
         }

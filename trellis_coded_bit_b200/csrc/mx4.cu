@@ -7,13 +7,14 @@
 // nearest code, ties to the even one, magnitudes over 6 taken to 6.  A block
 // that holds an infinity or a NaN gets the scale byte 255 and codes 0.
 //
-// A thread takes 8 consecutive columns, 4 threads a block of 32, 16 threads a
-// rotation block of 128.  The scaling by a power of two is exact, so without
-// the rotation every code is the definition's.  With it the sums run in fp64:
-// a rotated value that fp32 sums put on the other side of a rounding border
-// would be off by a whole step of the format, and two code paths (or two
-// split orders) would then disagree by that step.  fp64 sums of 128 fp16
-// values are exact, those of bf16 and fp32 values to 2^-46 of the largest.
+// The scaling by a power of two is exact, so without the rotation every code is
+// the definition's.  With it a sum that fp32 rounds across a border of the
+// 4-bit rounding would put its code off by a whole step of the format, and two
+// ways to the same sum would disagree by that step.  So the rotation runs in
+// fp32 with a bound on its error, and where a value (or a block's largest)
+// lies within the bound of a border its warp repeats it in fp64, whose sums are
+// exact for 128 fp16 values and good to 2^-46 of the largest for bf16 and fp32
+// ones.  (A rotated zero has the code of +0.)
 #include "dtypes.cuh"
 #include "exl3_device.cuh"
 #include "exl3_host.h"
@@ -75,15 +76,6 @@ __device__ __forceinline__ float inverse_scale32(int byte)
     return byte >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
 }
 
-// A double as the fp32 value that rounds to 4 bits the same way: truncated,
-// with the last bit set if anything was cut off, so that a value beside a
-// border or a tie stays beside it.
-__device__ __forceinline__ float sticky32(double v)
-{
-    const float f = __double2float_rz(v);
-    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
-
 // Codes and scale byte of this thread's 8 columns of a block of 32 (4 lanes).
 __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int *byte)
 {
@@ -105,132 +97,252 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int *byte)
     return codes8(r);
 }
 
-__device__ __forceinline__ uint32_t quantize8(const double (&v)[8], int *byte)
-{
-    uint64_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t a = (uint64_t)__double_as_longlong(v[i]) & 0x7fffffffffffffffull;
-        top = a > top ? a : top;
-    }
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-        const uint64_t o = __shfl_xor_sync(0xffffffffu, (unsigned long long)top, d);
-        top = o > top ? o : top;
-    }
-    const int b = scale_byte64(top);
-    *byte = b;
-    if (b == 255)
-        return 0u;
-    const double inv = __longlong_as_double((long long)(1023 + 127 - b) << 52);
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        r[i] = sticky32(v[i] * inv);
-    return codes8(r);
-}
-
-// x' of this thread's 8 columns: the 128-point Hadamard over 16 lanes, three
-// stages in registers and four across lanes.
-__device__ __forceinline__ void rotate8(double (&v)[8])
-{
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if ((i & h) == 0) {
-                const double a = v[i], b = v[i + h];
-                v[i] = a + b;
-                v[i + h] = a - b;
-            }
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
-        const bool upper = (threadIdx.x & m) != 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double o = __shfl_xor_sync(0xffffffffu, v[i], m);
-            v[i] = upper ? o - v[i] : v[i] + o;
-        }
-    }
-    const double s = 0.088388347648318440550;  // 1/sqrt(128)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] *= s;
-}
-
 struct Mx4QuantParams {
     const void *x;
     const __half *signs;
     const int32_t *positions;  // row r goes to rows positions[r topk ..] (null: to row r)
     uint8_t *codes, *scales;
     int64_t rows, out_rows;
-    int groups;                // k / 8: threads per row
+    int blocks;                // k / 32
     int topk, stride;          // stride: bytes of a row of scales
 };
 
-// A warp takes 32 consecutive groups of 8 columns of the matrix read as one
-// long row; the 4 (or 16) threads of a block never straddle two rows, since
-// a row is a multiple of 32 (128 with ROT) columns.
-template <typename T, bool ROT>
+// Calls f with each of the rows that row `row` goes to.
+template <typename F>
+__device__ __forceinline__ void for_each_row(const Mx4QuantParams &p, int64_t row, F f)
+{
+    if (!p.positions) {
+        f(row);
+        return;
+    }
+    for (int j = 0; j < p.topk; ++j) {
+        const int64_t to = p.positions[row * p.topk + j];
+        if (to >= 0 && to < p.out_rows)
+            f(to);
+    }
+}
+
+// Scale of block b of a row; behind the last block also the unused bytes.
+__device__ __forceinline__ void store_scale(const Mx4QuantParams &p, int64_t row, int b, int byte)
+{
+    uint8_t *s = p.scales + row * p.stride + b;
+    *s = (uint8_t)byte;
+    if (b + 1 == p.blocks)
+        for (int i = b + 1; i < p.stride; ++i)
+            *++s = 0;
+}
+
+// Without rotation: a thread takes 8 consecutive columns, 4 threads a block; a
+// warp 32 consecutive groups of the matrix read as one long row (a row is a
+// multiple of 32 columns, so no block straddles two).
+template <typename T>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams p)
 {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t total = p.rows * p.groups;
+    const int groups = p.blocks * 4;
+    const int64_t total = p.rows * groups;
     const int64_t stride = (int64_t)gridDim.x * blockDim.x;
     // rounded up to whole warps: every lane takes part in the shuffles
     for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x - (threadIdx.x & 31); g0 < total; g0 += stride) {
         const int64_t g = g0 + (threadIdx.x & 31);
         const bool live = g < total;
-        const int64_t row = live ? g / p.groups : 0;
-        const int c = live ? (int)(g - row * p.groups) : 0;
+        const int64_t row = live ? g / groups : 0;
+        const int c = live ? (int)(g - row * groups) : 0;
         float v[8];
-        load8<T>((const T *)p.x + (row * p.groups + c) * 8, v);
-        int byte;
-        uint32_t code;
-        if constexpr (ROT) {
-            double d[8];
+        load8<T>((const T *)p.x + (row * groups + c) * 8, v);
+        if (p.signs) {
+            float s[8];
+            load8<__half>(p.signs + c * 8, s);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                d[i] = (double)v[i];
-            if (p.signs) {
-                float s[8];
-                load8<__half>(p.signs + c * 8, s);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    d[i] *= (double)s[i];
-            }
-            rotate8(d);
-            code = quantize8(d, &byte);
-        } else {
-            if (p.signs) {
-                float s[8];
-                load8<__half>(p.signs + c * 8, s);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] *= s[i];
-            }
-            code = quantize8(v, &byte);
+                v[i] *= s[i];
         }
+        int byte;
+        const uint32_t code = quantize8(v, &byte);
         if (!live)
             continue;
-        const int n = p.positions ? p.topk : 1;
-        for (int j = 0; j < n; ++j) {
-            int64_t to = row;
-            if (p.positions) {
-                to = p.positions[row * p.topk + j];
-                if (to < 0 || to >= p.out_rows)
-                    continue;
+        for_each_row(p, row, [&](int64_t to) {
+            reinterpret_cast<uint32_t *>(p.codes)[to * groups + c] = code;
+            if ((c & 3) == 0)
+                store_scale(p, to, c >> 2, byte);
+        });
+    }
+}
+
+// ------------------------------------------------------ with the rotation ---
+//
+// A thread takes a block of 32 columns (no exchange for its largest magnitude,
+// one 16-byte store of codes), 4 lanes the 128 of a rotation: five butterfly
+// stages in registers, two across lanes.
+
+// 32-point Sylvester Hadamard in registers, then over the lanes 1 and 2 apart.
+template <typename F>
+__device__ __forceinline__ void rotate32x4(F (&v)[32])
+{
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if ((i & h) == 0) {
+                const F a = v[i], b = v[i + h];
+                v[i] = a + b;
+                v[i + h] = a - b;
             }
-            reinterpret_cast<uint32_t *>(p.codes)[to * p.groups + c] = code;
-            if ((c & 3) == 0) {
-                uint8_t *sc = p.scales + to * p.stride + (c >> 2);
-                *sc = (uint8_t)byte;
-                if (c + 4 == p.groups)  // the row's last block: the unused bytes behind it
-                    for (int i = (c >> 2) + 1; i < p.stride; ++i)
-                        *++sc = 0;
-            }
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const bool upper = (threadIdx.x & m) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const F o = __shfl_xor_sync(0xffffffffu, v[i], m);
+            v[i] = upper ? o - v[i] : v[i] + o;
         }
+    }
+}
+
+// Codes of zero magnitude without their sign.
+__device__ __forceinline__ uint32_t unsigned_zeros(uint32_t code)
+{
+    const uint32_t m = code & 0x77777777u;
+    const uint32_t some = (m | m >> 1 | m >> 2) & 0x11111111u;
+    return m | (code & (some << 3));
+}
+
+// A double as the fp32 value that rounds to 4 bits the same way: truncated,
+// with the last bit set if anything was cut off, so that a value beside a
+// border or a tie stays beside it.
+__device__ __forceinline__ float sticky32(double v)
+{
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// A block in fp64, read again (x, signs: the thread's 32 columns).  A call of
+// its own: about one warp in 70 of normal data comes here.
+template <typename T>
+__device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *signs, int *byte)
+{
+    double v[32];
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+        float f[8];
+        load8<T>(x + c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[c + i] = (double)f[i];
+        if (signs) {
+            load8<__half>(signs + c, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[c + i] *= (double)f[i];
+        }
+    }
+    rotate32x4(v);
+    uint64_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] *= 0.088388347648318440550;  // 1/sqrt(128)
+        const uint64_t a = (uint64_t)__double_as_longlong(v[i]) & 0x7fffffffffffffffull;
+        top = a > top ? a : top;
+    }
+    const int b = scale_byte64(top);
+    *byte = b;
+    if (b == 255)
+        return make_uint4(0u, 0u, 0u, 0u);
+    const double inv = __longlong_as_double((long long)(1023 + 127 - b) << 52);
+    uint32_t out[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[i] = sticky32(v[8 * c + i] * inv);
+        out[c] = unsigned_zeros(codes8(r));
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Error bound.  Each of the 7 stages rounds values whose magnitudes, over the
+// tree of one output, add up to at most S = sum |x .* signs| (128 values), by
+// 2^-24 each: 7 2^-24 S, and 2^-24 S for the products with the signs.  The
+// factor 1/sqrt(128) 2^-e and the product with it are off by 2^-24 of a result
+// below 8 each: 2^-20.  Together, in units of the scale,
+//     |r - exact| <= 2^-21 S 2^-e / sqrt(128) + 2^-20,
+// of which `slack` is twice the first part, for the roundings of S and slack.
+template <typename T>
+__global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4QuantParams p)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t total = p.rows * p.blocks;
+    const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x - (threadIdx.x & 31); g0 < total; g0 += stride) {
+        const int64_t g = g0 + (threadIdx.x & 31);
+        const bool live = g < total;
+        const int64_t row = live ? g / p.blocks : 0;
+        const int c = live ? (int)(g - row * p.blocks) : (int)(threadIdx.x & 3);
+        const T *const x = (const T *)p.x + (row * p.blocks + c) * 32;
+        const __half *const signs = p.signs ? p.signs + c * 32 : nullptr;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            float f[8];
+            load8<T>(x + i, f);
+            if (signs) {
+                float s[8];
+                load8<__half>(signs + i, s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] *= s[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i + j] = f[j];
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            sum += fabsf(v[i]);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        rotate32x4(v);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            top = fmaxf(top, fabsf(v[i]));
+        const float s = 0.08838834764831845f;  // 1/sqrt(128)
+        int byte = scale_byte32(__float_as_uint(top * s));
+        uint4 code = make_uint4(0u, 0u, 0u, 0u);
+        // zeros are exact; what leaves fp32's range or the scales' takes fp64
+        bool sure = sum == 0.f;
+        if (!sure && byte >= 1 && byte <= 253 && sum < 1e38f) {
+            const float inv = inverse_scale32(byte) * s;
+            const float slack = fmaf(0x1p-20f * sum, inv, 0x1p-20f);
+            const float most = top * inv;
+            uint32_t out[4], differ = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo[8], hi[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float r = v[8 * i + j] * inv;
+                    lo[j] = r - slack;
+                    hi[j] = r + slack;
+                }
+                out[i] = unsigned_zeros(codes8(lo));
+                differ |= out[i] ^ unsigned_zeros(codes8(hi));
+            }
+            code = make_uint4(out[0], out[1], out[2], out[3]);
+            sure = differ == 0 && most > 4.f + slack && most < 8.f - slack;
+        }
+        if (!__all_sync(0xffffffffu, sure))
+            code = quantize_block_fp64<T>(x, signs, &byte);
+        if (!live)
+            continue;
+        for_each_row(p, row, [&](int64_t to) {
+            reinterpret_cast<uint4 *>(p.codes)[to * p.blocks + c] = code;
+            store_scale(p, to, c, byte);
+        });
     }
 }
 
@@ -269,17 +381,19 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *__r
     }
 }
 
-static unsigned mx4_grid(int64_t threads)
+static unsigned mx4_grid(int64_t threads, int block)
 {
-    const int64_t blocks = (threads + 255) / 256;
+    const int64_t blocks = (threads + block - 1) / block;
     return (unsigned)(blocks < 148 * 32 ? blocks : 148 * 32);
 }
 
 template <typename T>
 static exl3_status launch_quantize(const Mx4QuantParams &p, bool rotate, cudaStream_t s)
 {
-    auto kern = rotate ? mx4_quantize_kernel<T, true> : mx4_quantize_kernel<T, false>;
-    if (launch_kernel(kern, dim3(mx4_grid(p.rows * p.groups)), dim3(256), 0, s, p) != cudaSuccess)
+    const cudaError_t e =
+        rotate ? launch_kernel(mx4_rotate_quantize_kernel<T>, dim3(mx4_grid(p.rows * p.blocks, 128)), dim3(128), 0, s, p)
+               : launch_kernel(mx4_quantize_kernel<T>, dim3(mx4_grid(p.rows * p.blocks * 4, 256)), dim3(256), 0, s, p);
+    if (e != cudaSuccess)
         return EXL3_ERR_CUDA;
     return launch_status();
 }
@@ -324,7 +438,7 @@ extern "C" exl3_status exl3_mx4_quantize(const void *x, int dtype, const void *s
     p.scales = scales;
     p.rows = rows;
     p.out_rows = to_rows;
-    p.groups = (int)(k / 8);
+    p.blocks = (int)(k / 32);
     p.topk = positions ? (int)topk : 1;
     p.stride = (int)mx4_scale_stride(k);
     cudaStream_t s = (cudaStream_t)stream;
@@ -350,7 +464,7 @@ extern "C" exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *
         ranges_overlap(scales, (size_t)(rows * mx4_scale_stride(k)), w, wb))
         return EXL3_ERR_INVALID_ARG;
     const int groups = (int)(k / 8), stride = (int)mx4_scale_stride(k);
-    const dim3 grid(mx4_grid(rows * groups)), block(256);
+    const dim3 grid(mx4_grid(rows * groups, 256)), block(256);
     cudaStream_t s = (cudaStream_t)stream;
     const uint32_t *c = (const uint32_t *)codes;
     cudaError_t e;

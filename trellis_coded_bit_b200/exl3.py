@@ -431,65 +431,83 @@ def exl3_ldlq(w, h, K, trellis=None, w_hat=None, workspace=None, stream=None):
 
 
 # ------------------------------------------- 4-bit matrices and experts ---
-
-def _typed(t, name, types=DTYPES):
-    """Pointer and exl3_dtype of a tensor of one of `types`."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in types:
-        raise TypeError("%s must be a CUDA tensor of %s" % (name, " or ".join(str(d) for d in types)))
-    return _dev(t, t.dtype, name), DTYPES[t.dtype]
-
+#
+# A decoding step makes these calls by the dozen, each of a few microseconds on
+# the GPU, so their checks are written to cost little: one pass over a call's
+# tensors, no context manager and no stream object unless one is needed.
 
 _HALF_TYPES = (torch.float16, torch.bfloat16)
 
 
+def _arg(t, dtype, name, device):
+    """Address of a contiguous CUDA tensor of `dtype` on device number `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != device:
+        raise ValueError("tensors of one call must be on one device: %s is on %s, not cuda:%d"
+                         % (name, t.device, device))
+    return t.data_ptr()
+
+
+def _device(t, name, types):
+    """Device number and exl3_dtype of a call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype not in types:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in types), t.dtype))
+    return t.get_device(), DTYPES.get(t.dtype)
+
+
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != shape:
         raise ValueError("%s must be %s, is %s" % (name, " x ".join(str(s) for s in shape), tuple(t.shape)))
 
 
-def _output(t, shape, dtype, like, name):
-    """The given output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _shape(t, shape, name)
-    return t
+def _call(name, device, stream, *args):
+    """Calls the library on `stream`, or on the current stream of `device`,
+    with that device current."""
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == device:
+        s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            status = fn(*args, s.cuda_stream)
+    if status != EXL3_OK:
+        raise Exl3Error(status, name)
 
 
-def _same_device(*tensors):
-    """The one device of a call's tensors (None entries are skipped)."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError("tensors of one call must be on one device, got %s" % sorted(str(d) for d in devices))
-    return devices.pop()
-
-
-def _call(name, device, stream, args):
-    """Calls the library with `device` current, on `stream` or its current stream."""
-    with torch.cuda.device(device):
-        _check(getattr(load(), name)(*args, _stream(stream)), name)
-
-
-def _workspace(t, name):
+def _workspace(t, name, device):
     if t is None:
         raise ValueError("%s needs a workspace (see new_workspace / %s_workspace_size)" % (name, name))
-    return _dev(t, torch.uint8, "workspace")
+    return _arg(t, torch.uint8, "workspace", device)
 
 
 def exl3_mx4_scale_stride(k):
-    """Bytes of a row of scales of a 4-bit matrix with k columns."""
-    return int(load().exl3_mx4_scale_stride(k))
+    """Bytes of a row of scales of a 4-bit matrix with k columns (0: no valid k)."""
+    return 0 if k <= 0 or k % 32 or k > 1 << 22 else (k + 511) // 512 * 16
+
+
+def _mx4_stride(k):
+    stride = exl3_mx4_scale_stride(k)
+    if stride == 0:
+        raise ValueError("k = %d must be a multiple of 32 from 32 to 2^22" % k)
+    return stride
 
 
 def _mx4_operand(codes, scales, dims, what):
-    """Checks a 4-bit operand of `dims` leading dimensions; returns (shape[:-1], k)."""
-    if codes.dim() != dims + 1:
+    """Checks a 4-bit operand's shapes; returns its leading dimensions and k."""
+    shape = tuple(codes.shape)
+    if len(shape) != dims + 1:
         raise ValueError("%s codes must have %d dimensions" % (what, dims + 1))
-    k = codes.shape[-1] * 2
-    stride = exl3_mx4_scale_stride(k)
-    if stride == 0:
-        raise ValueError("%s: k = %d must be a positive multiple of 32" % (what, k))
-    _shape(scales, tuple(codes.shape[:-1]) + (stride,), what + " scales")
-    return tuple(codes.shape[:-1]), k
+    k = shape[-1] * 2
+    _shape(scales, shape[:-1] + (_mx4_stride(k),), what + " scales")
+    return shape[:-1], k
 
 
 def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None, codes=None, scales=None,
@@ -501,12 +519,7 @@ def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None
     if x.dim() != 2:
         raise ValueError("x must be rows x k")
     rows, k = x.shape
-    px, dtype = _typed(x, "x")
-    stride = exl3_mx4_scale_stride(k)
-    if stride == 0:
-        raise ValueError("k = %d must be a positive multiple of 32" % k)
-    if signs is not None:
-        _shape(signs, (k,), "signs")
+    stride = _mx4_stride(k)
     topk, to = 1, rows
     if positions is not None:
         if positions.dim() != 2 or positions.shape[0] != rows:
@@ -515,24 +528,34 @@ def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None
         if out_rows is None:
             raise ValueError("positions need out_rows")
         to = int(out_rows)
-    codes = _output(codes, (to, k // 2), torch.uint8, x, "codes")
-    scales = _output(scales, (to, stride), torch.uint8, x, "scales")
-    device = _same_device(x, signs, positions, codes, scales)
-    _call("exl3_mx4_quantize", device, stream,
-          (px, dtype, _ptr_or_none(signs, torch.float16, "signs"), 1 if rotate else 0,
-           _ptr_or_none(positions, torch.int32, "positions"), topk, to, _dev(codes, torch.uint8, "codes"),
-           _dev(scales, torch.uint8, "scales"), rows, k))
+    device, dtype = _device(x, "x", DTYPES)
+    if signs is not None:
+        _shape(signs, (k,), "signs")
+    if codes is None:
+        codes = torch.empty((to, k // 2), dtype=torch.uint8, device=x.device)
+    else:
+        _shape(codes, (to, k // 2), "codes")
+    if scales is None:
+        scales = torch.empty((to, stride), dtype=torch.uint8, device=x.device)
+    else:
+        _shape(scales, (to, stride), "scales")
+    _call("exl3_mx4_quantize", device, stream, _arg(x, x.dtype, "x", device), dtype,
+          None if signs is None else _arg(signs, torch.float16, "signs", device), 1 if rotate else 0,
+          None if positions is None else _arg(positions, torch.int32, "positions", device), topk, to,
+          _arg(codes, torch.uint8, "codes", device), _arg(scales, torch.uint8, "scales", device), rows, k)
     return codes, scales
 
 
 def exl3_mx4_dequantize(codes, scales, dtype=torch.float16, out=None, stream=None):
     """The values of a 4-bit matrix, rows x k, as fp16, bf16 or fp32."""
     (rows,), k = _mx4_operand(codes, scales, 1, "matrix")
-    out = _output(out, (rows, k), dtype, codes, "out")
-    po, dt = _typed(out, "out")
-    device = _same_device(codes, scales, out)
-    _call("exl3_mx4_dequantize", device, stream,
-          (_dev(codes, torch.uint8, "codes"), _dev(scales, torch.uint8, "scales"), po, dt, rows, k))
+    if out is None:
+        out = torch.empty((rows, k), dtype=dtype, device=codes.device)
+    else:
+        _shape(out, (rows, k), "out")
+    device, dt = _device(out, "out", DTYPES)
+    _call("exl3_mx4_dequantize", device, stream, _arg(codes, torch.uint8, "codes", device),
+          _arg(scales, torch.uint8, "scales", device), _arg(out, out.dtype, "out", device), dt, rows, k)
     return out
 
 
@@ -546,13 +569,15 @@ def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None,
     (n,), kw = _mx4_operand(wc, ws, 1, "w")
     if kw != k:
         raise ValueError("x has k = %d, w has %d" % (k, kw))
-    y = _output(y, (m, n), dtype, xc, "y")
-    py, dt = _typed(y, "y", _HALF_TYPES)
-    pw = _workspace(workspace, "exl3_mx4_matmul")
-    device = _same_device(xc, xs, wc, ws, y, workspace)
-    _call("exl3_mx4_matmul", device, stream,
-          (_dev(xc, torch.uint8, "x codes"), _dev(xs, torch.uint8, "x scales"), _dev(wc, torch.uint8, "w codes"),
-           _dev(ws, torch.uint8, "w scales"), py, dt, m, k, n, pw, workspace.numel()))
+    if y is None:
+        y = torch.empty((m, n), dtype=dtype, device=xc.device)
+    else:
+        _shape(y, (m, n), "y")
+    device, dt = _device(y, "y", _HALF_TYPES)
+    _call("exl3_mx4_matmul", device, stream, _arg(xc, torch.uint8, "x codes", device),
+          _arg(xs, torch.uint8, "x scales", device), _arg(wc, torch.uint8, "w codes", device),
+          _arg(ws, torch.uint8, "w scales", device), _arg(y, y.dtype, "y", device), dt, m, k, n,
+          _workspace(workspace, "exl3_mx4_matmul", device), workspace.numel())
     return y
 
 
@@ -566,18 +591,20 @@ def exl3_mx4_linear(x, wc, ws, signs=None, rotate=False, y=None, workspace=None,
     if x.dim() != 2:
         raise ValueError("x must be m x k")
     m, k = x.shape
-    px, dt = _typed(x, "x", _HALF_TYPES)
     (n,), kw = _mx4_operand(wc, ws, 1, "w")
     if kw != k:
         raise ValueError("x has k = %d, w has %d" % (k, kw))
+    device, dt = _device(x, "x", _HALF_TYPES)
     if signs is not None:
         _shape(signs, (k,), "signs")
-    y = _output(y, (m, n), x.dtype, x, "y")
-    pw = _workspace(workspace, "exl3_mx4_linear")
-    device = _same_device(x, signs, wc, ws, y, workspace)
-    _call("exl3_mx4_linear", device, stream,
-          (px, dt, _ptr_or_none(signs, torch.float16, "signs"), 1 if rotate else 0, _dev(wc, torch.uint8, "w codes"),
-           _dev(ws, torch.uint8, "w scales"), _dev(y, x.dtype, "y"), m, k, n, pw, workspace.numel()))
+    if y is None:
+        y = torch.empty((m, n), dtype=x.dtype, device=x.device)
+    else:
+        _shape(y, (m, n), "y")
+    _call("exl3_mx4_linear", device, stream, _arg(x, x.dtype, "x", device), dt,
+          None if signs is None else _arg(signs, torch.float16, "signs", device), 1 if rotate else 0,
+          _arg(wc, torch.uint8, "w codes", device), _arg(ws, torch.uint8, "w scales", device),
+          _arg(y, x.dtype, "y", device), m, k, n, _workspace(workspace, "exl3_mx4_linear", device), workspace.numel())
     return y
 
 
@@ -593,14 +620,16 @@ def exl3_mx4_matmul_experts(xc, xs, offsets, wc, ws, dtype=torch.float16, y=None
     if kw != k:
         raise ValueError("x has k = %d, w has %d" % (k, kw))
     _shape(offsets, (experts + 1,), "offsets")
-    y = _output(y, (rows, n), dtype, xc, "y")
-    py, dt = _typed(y, "y", _HALF_TYPES)
-    pw = _workspace(workspace, "exl3_mx4_matmul_experts")
-    device = _same_device(xc, xs, offsets, wc, ws, y, workspace)
-    _call("exl3_mx4_matmul_experts", device, stream,
-          (_dev(xc, torch.uint8, "x codes"), _dev(xs, torch.uint8, "x scales"), _dev(offsets, torch.int32, "offsets"),
-           _dev(wc, torch.uint8, "w codes"), _dev(ws, torch.uint8, "w scales"), py, dt, rows, k, n, experts, pw,
-           workspace.numel()))
+    if y is None:
+        y = torch.empty((rows, n), dtype=dtype, device=xc.device)
+    else:
+        _shape(y, (rows, n), "y")
+    device, dt = _device(y, "y", _HALF_TYPES)
+    _call("exl3_mx4_matmul_experts", device, stream, _arg(xc, torch.uint8, "x codes", device),
+          _arg(xs, torch.uint8, "x scales", device), _arg(offsets, torch.int32, "offsets", device),
+          _arg(wc, torch.uint8, "w codes", device), _arg(ws, torch.uint8, "w scales", device),
+          _arg(y, y.dtype, "y", device), dt, rows, k, n, experts,
+          _workspace(workspace, "exl3_mx4_matmul_experts", device), workspace.numel())
     return y
 
 
@@ -614,20 +643,25 @@ def exl3_moe_sort(ids, experts, offsets=None, positions=None, workspace=None, st
     if ids.dim() != 2:
         raise ValueError("ids must be tokens x topk")
     tokens, topk = ids.shape
-    offsets = _output(offsets, (experts + 1,), torch.int32, ids, "offsets")
-    positions = _output(positions, (tokens, topk), torch.int32, ids, "positions")
-    pw = _workspace(workspace, "exl3_moe_sort")
-    device = _same_device(ids, offsets, positions, workspace)
-    _call("exl3_moe_sort", device, stream,
-          (_dev(ids, torch.int32, "ids"), tokens, topk, experts, _dev(offsets, torch.int32, "offsets"),
-           _dev(positions, torch.int32, "positions"), pw, workspace.numel()))
+    device, _ = _device(ids, "ids", (torch.int32,))
+    if offsets is None:
+        offsets = torch.empty((experts + 1,), dtype=torch.int32, device=ids.device)
+    else:
+        _shape(offsets, (experts + 1,), "offsets")
+    if positions is None:
+        positions = torch.empty((tokens, topk), dtype=torch.int32, device=ids.device)
+    else:
+        _shape(positions, (tokens, topk), "positions")
+    _call("exl3_moe_sort", device, stream, _arg(ids, torch.int32, "ids", device), tokens, topk, experts,
+          _arg(offsets, torch.int32, "offsets", device), _arg(positions, torch.int32, "positions", device),
+          _workspace(workspace, "exl3_moe_sort", device), workspace.numel())
     return offsets, positions
 
 
-def _positions(positions, tokens):
+def _topk(positions, tokens):
     if positions.dim() != 2 or (tokens is not None and positions.shape[0] != tokens):
         raise ValueError("positions must be tokens x topk")
-    return _dev(positions, torch.int32, "positions"), positions.shape[1]
+    return positions.shape[1]
 
 
 def exl3_moe_gather(x, positions, out=None, out_rows=None, stream=None):
@@ -636,14 +670,15 @@ def exl3_moe_gather(x, positions, out=None, out_rows=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be tokens x h")
     tokens, h = x.shape
-    pp, topk = _positions(positions, tokens)
-    px, dt = _typed(x, "x")
+    topk = _topk(positions, tokens)
+    device, dt = _device(x, "x", DTYPES)
     if out is None:
         out = torch.empty((tokens * topk if out_rows is None else int(out_rows), h), dtype=x.dtype, device=x.device)
     elif out.dim() != 2 or out.shape[1] != h:
         raise ValueError("out must be rows x h")
-    device = _same_device(x, positions, out)
-    _call("exl3_moe_gather", device, stream, (px, dt, pp, tokens, topk, h, out.shape[0], _dev(out, x.dtype, "out")))
+    _call("exl3_moe_gather", device, stream, _arg(x, x.dtype, "x", device), dt,
+          _arg(positions, torch.int32, "positions", device), tokens, topk, h, out.shape[0],
+          _arg(out, x.dtype, "out", device))
     return out
 
 
@@ -652,15 +687,19 @@ def exl3_moe_combine(ys, positions, weights=None, y=None, stream=None):
     if ys.dim() != 2:
         raise ValueError("ys must be rows x h")
     rows, h = ys.shape
-    pp, topk = _positions(positions, None)
+    topk = _topk(positions, None)
     tokens = positions.shape[0]
-    py, dt = _typed(ys, "ys")
+    device, dt = _device(ys, "ys", DTYPES)
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
-    y = _output(y, (tokens, h), ys.dtype, ys, "y")
-    device = _same_device(ys, positions, weights, y)
-    _call("exl3_moe_combine", device, stream,
-          (py, dt, pp, _ptr_or_none(weights, torch.float32, "weights"), tokens, topk, h, rows, _dev(y, ys.dtype, "y")))
+    if y is None:
+        y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
+    else:
+        _shape(y, (tokens, h), "y")
+    _call("exl3_moe_combine", device, stream, _arg(ys, ys.dtype, "ys", device), dt,
+          _arg(positions, torch.int32, "positions", device),
+          None if weights is None else _arg(weights, torch.float32, "weights", device), tokens, topk, h, rows,
+          _arg(y, ys.dtype, "y", device))
     return y
 
 
@@ -671,16 +710,22 @@ def exl3_moe_combine_grad(dy, ys, positions, weights=None, dys=None, dweights=No
         raise ValueError("dy must be tokens x h and ys rows x h")
     tokens, h = dy.shape
     rows = ys.shape[0]
-    pp, topk = _positions(positions, tokens)
-    pd, dt = _typed(dy, "dy")
+    topk = _topk(positions, tokens)
+    device, dt = _device(dy, "dy", DTYPES)
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
-    dys = _output(dys, (rows, h), dy.dtype, dy, "dys")
-    dweights = _output(dweights, (tokens, topk), torch.float32, dy, "dweights")
-    device = _same_device(dy, ys, positions, weights, dys, dweights)
-    _call("exl3_moe_combine_grad", device, stream,
-          (pd, _dev(ys, dy.dtype, "ys"), dt, pp, _ptr_or_none(weights, torch.float32, "weights"), tokens, topk, h, rows,
-           _dev(dys, dy.dtype, "dys"), _dev(dweights, torch.float32, "dweights")))
+    if dys is None:
+        dys = torch.empty((rows, h), dtype=dy.dtype, device=dy.device)
+    else:
+        _shape(dys, (rows, h), "dys")
+    if dweights is None:
+        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=dy.device)
+    else:
+        _shape(dweights, (tokens, topk), "dweights")
+    _call("exl3_moe_combine_grad", device, stream, _arg(dy, dy.dtype, "dy", device),
+          _arg(ys, dy.dtype, "ys", device), dt, _arg(positions, torch.int32, "positions", device),
+          None if weights is None else _arg(weights, torch.float32, "weights", device), tokens, topk, h, rows,
+          _arg(dys, dy.dtype, "dys", device), _arg(dweights, torch.float32, "dweights", device))
     return dys, dweights
 
 
