@@ -77,7 +77,7 @@ struct MxParams {
     const int32_t *offsets;     // [experts + 1] first token row of each expert, or null: one expert, all rows
     void *y;
     float *partials;            // [2 CTAs][TN / 4][128][4]
-    uint32_t *counters;         // [CTAs]
+    uint32_t *counters;         // [split tiles, fewer than workers][CG]
     uint32_t *status;
     int64_t rows;               // token rows
     int n, k, kb_count, experts, stride;
@@ -285,19 +285,26 @@ __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const uint32_t *f
 // ------------------------------------------------------------ schedule ---
 //
 // T tiles on G workers (a CTA, or the pair of CTAs that shares a tile).  The
-// last T mod G tiles are split: their units (tile, 256 columns) in order, an
-// equal share for each worker, done first so that the sums meet while the
-// whole tiles run.  Then worker c takes the whole tiles c, c + G, ...:
-// at any time the workers are on neighbouring tiles, which share weights, so
-// that these come from memory once.  (With contiguous shares instead, 74 pairs
-// held 74 different rows of weights: 2048 x 8192 x 18944 took 241 us, waiting
-// 3.4 us for each copy.)
+// last T mod G tiles are split over the workers along k and done first, so that
+// the sums meet while the whole tiles run.  Then worker c takes the whole tiles
+// c, c + G, ...: at any time the workers are on neighbouring tiles, which share
+// weights, so that these come from memory once.  (With contiguous shares of the
+// tiles instead, 74 pairs held 74 different rows of weights: 2048 x 8192 x 18944
+// took 241 us, waiting 3.4 us for each copy.)
+//
+// Split tiles: `even` gives each tile floor or ceil(W / tiles) workers of its
+// own, so a worker has one segment and waits for one sum; otherwise the units
+// (tile, 256 columns) in order are cut into equal shares, and a worker may end
+// one tile and begin the next.  Even is taken where its longest segment is at
+// most one unit longer (4096 channels, k = 4096: 4 units either way).
 struct MxSched {
     uint32_t worker, G, KB;
     uint32_t whole;      // whole tiles of each worker
     uint32_t split0;     // first split tile
-    uint32_t U, W;       // units of the split tiles, workers that share them
-    uint32_t u0, u1;     // this worker's
+    uint32_t splits;     // split tiles
+    uint32_t U, W;       // their units, the workers that share them
+    uint32_t u0, u1;     // this worker's units
+    bool even;
     int split_segs, segs;
 };
 
@@ -307,22 +314,37 @@ struct MxSeg {
     int k0, k1;
 };
 
+// (32 bits are enough: there are fewer split tiles than workers, so the
+// products stay below workers^2 2^22/256.)
 __device__ __forceinline__ uint32_t mx_begin(const MxSched &m, uint32_t c)
 {
-    return (uint32_t)((uint64_t)c * m.U / m.W);
+    return c * m.U / m.W;
 }
 
-// The worker that owns unit u of the split tiles.
-__device__ __forceinline__ uint32_t mx_owner(const MxSched &m, uint32_t u)
+// even: the first worker of split tile i.
+__device__ __forceinline__ uint32_t mx_first_worker(const MxSched &m, uint32_t i)
 {
-    return (uint32_t)((((uint64_t)u + 1) * m.W - 1) / m.U);
+    return i * m.W / m.splits;
 }
 
-// Partial slot of worker c's segment of the split tile that begins at unit tb:
-// its first segment uses 2c, its second 2c + 1.
-__device__ __forceinline__ uint32_t mx_slot(const MxSched &m, uint32_t c, uint32_t tb)
+// The workers of split tile i: [lo, lo + n).
+__device__ __forceinline__ void mx_workers(const MxSched &m, uint32_t i, uint32_t &lo, int &n)
 {
-    return mx_begin(m, c) >= tb ? 2 * c : 2 * c + 1;
+    if (m.even) {
+        lo = mx_first_worker(m, i);
+        n = (int)(mx_first_worker(m, i + 1) - lo);
+    } else {
+        const uint32_t b = i * m.KB;
+        lo = ((b + 1) * m.W - 1) / m.U;
+        n = (int)(((b + m.KB) * m.W - 1) / m.U - lo) + 1;
+    }
+}
+
+// Partial slot of worker c's segment of split tile i: its first segment uses
+// 2c, its second 2c + 1.
+__device__ __forceinline__ uint32_t mx_slot(const MxSched &m, uint32_t c, uint32_t i)
+{
+    return m.even || mx_begin(m, c) >= i * m.KB ? 2 * c : 2 * c + 1;
 }
 
 __device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint32_t workers, uint32_t worker)
@@ -333,15 +355,28 @@ __device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint
     m.KB = KB;
     m.whole = tiles / workers;
     m.split0 = m.whole * workers;
-    m.U = (tiles - m.split0) * KB;
+    m.splits = tiles - m.split0;
+    m.U = m.splits * KB;
     // no more workers than units: with an empty share between two others a
     // tile's segments would be miscounted
     m.W = m.U < workers ? m.U : workers;
     m.u0 = m.u1 = 0;
     m.split_segs = 0;
+    m.even = false;
     if (worker < m.W) {
-        m.u0 = mx_begin(m, worker);
-        m.u1 = mx_begin(m, worker + 1);
+        const uint32_t least = m.W / m.splits;  // workers of a tile, at least
+        m.even = (KB + least - 1) / least <= (m.U + m.W - 1) / m.W + 1;
+        if (m.even) {
+            const uint32_t i = ((worker + 1) * m.splits - 1) / m.W;
+            uint32_t lo;
+            int n;
+            mx_workers(m, i, lo, n);
+            m.u0 = i * KB + (worker - lo) * KB / (uint32_t)n;
+            m.u1 = i * KB + (worker - lo + 1) * KB / (uint32_t)n;
+        } else {
+            m.u0 = mx_begin(m, worker);
+            m.u1 = mx_begin(m, worker + 1);
+        }
         m.split_segs = (int)((m.u1 - 1) / KB - m.u0 / KB) + 1;
     }
     m.segs = m.split_segs + (int)m.whole;
@@ -508,12 +543,13 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     }
 
     // A split tile: fp32 partials to the workspace, [4 columns][lane][4]
-    const uint32_t tb = (g.t - sched.split0) * sched.KB;
-    const uint32_t c_lo = mx_owner(sched, tb);
-    const int nseg = (int)(mx_owner(sched, tb + sched.KB - 1) - c_lo) + 1;
+    const uint32_t split = g.t - sched.split0;
+    uint32_t c_lo;
+    int nseg;
+    mx_workers(sched, split, c_lo, nseg);
     constexpr size_t kSlot = (size_t)TN * kMxBM;
     const size_t lane_at = (size_t)(c0 / 4) * (4 * kMxBM) + (size_t)(quarter * 32 + lane) * 4;
-    float *const mine = p.partials + ((size_t)mx_slot(sched, sched.worker, tb) * CG + rank) * kSlot + lane_at;
+    float *const mine = p.partials + ((size_t)mx_slot(sched, sched.worker, split) * CG + rank) * kSlot + lane_at;
 #pragma unroll 1
     for (int c = 0; c < cols; c += 16) {
         uint32_t b[16];
@@ -525,10 +561,11 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                        make_float4(__uint_as_float(b[4 * g]), __uint_as_float(b[4 * g + 1]),
                                    __uint_as_float(b[4 * g + 2]), __uint_as_float(b[4 * g + 3])));
     }
-    __threadfence();
     mx_epi_sync<TN, CG>();
     if (threadIdx.x == 32 * S::kEpiWarp0) {
-        uint32_t *counter = &p.counters[c_lo * CG + rank];
+        // the barrier orders the other threads' partials before this fence
+        __threadfence();
+        uint32_t *counter = &p.counters[split * CG + rank];
         const int last = atomicAdd(counter, 1u) == (uint32_t)(nseg - 1);
         if (last)
             *counter = 0u;  // every segment has arrived: re-arm for the next call
@@ -556,7 +593,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                 for (int j = 0; j < kAhead; ++j) {
                     if (j0 + j < nseg && j0 + j != own) {
                         const float *src = p.partials +
-                                           ((size_t)mx_slot(sched, c_lo + j0 + j, tb) * CG + rank) * kSlot + lane_at +
+                                           ((size_t)mx_slot(sched, c_lo + j0 + j, split) * CG + rank) * kSlot + lane_at +
                                            (size_t)(c / 4) * (4 * kMxBM);
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
@@ -618,7 +655,13 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     const uint32_t worker = blockIdx.x / CG;
-    if (threadIdx.x == 0) {
+    // Without experts the tiles are known at once, and the thread that issues
+    // the copies starts the first stages' weights before anything else: they do
+    // not depend on the kernel before (the tokens, and all else, wait for it).
+    const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
+    const bool early = CG == 1 && !p.offsets;
+    int pre = 0;  // stages begun early
+    if (threadIdx.x == 32 * kMxFeedWarp0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&bars.full[s], 1 + CG * S::kFeedWarps);  // the bytes, each CTA's scales
             mbar_init(&bars.empty[s], 1);
@@ -631,14 +674,41 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         bars.epi_abort = 0;
         bars.ticket = 0;
         fence_mbar_init();
+        if (early) {
+            const uint32_t tts = (uint32_t)((p.rows + TN - 1) / TN);
+            first[0] = 0;
+            first[1] = nts * tts;
+            const MxSched sched = mx_schedule(nts * tts, (uint32_t)p.kb_count, gridDim.x / CG, worker);
+            int rows[ST], cols[ST];
+#pragma unroll
+            for (int seg = 0, kb = 0, end = 0, wrow = 0, xrow = 0; pre < ST; ++kb, ++pre) {
+                while (kb >= end && seg < sched.segs) {
+                    const MxSeg g = mx_seg(sched, seg++);
+                    kb = g.k0;
+                    end = g.k1;
+                    wrow = (int)(g.t / tts) * kMxBM;
+                    xrow = (int)(g.t % tts) * TN;
+                }
+                if (kb >= end)
+                    break;
+                mbar_arrive_expect_tx(&bars.full[pre], kMxABytes + S::kBBytes);
+                tma_load_2d<CG>(aring + pre * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, smem_addr(&bars.full[pre]));
+                rows[pre] = xrow;
+                cols[pre] = kb * (kMxBK / 2);
+            }
+            grid_dep_wait();
+#pragma unroll
+            for (int s = 0; s < ST; ++s)
+                if (s < pre)
+                    tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, cols[s], rows[s], smem_addr(&bars.full[s]));
+        }
     }
     if (warp == kMxMmaWarp)
         mx_tmem_alloc<CG>(&bars.tmem_slot);
     grid_dep_wait();
     grid_dep_launch();
-    if (warp == 0) {
+    if (warp == 0 && !early) {
         // prefix sums of the experts' tiles
-        const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
         uint32_t run = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
             uint32_t v = 0;
@@ -807,8 +877,8 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             }
         };
         next();
-        uint32_t par = 1;
-        uint32_t issued = 0;  // stages that were ever filled: bits
+        uint32_t round = 0;  // of the ring
+        uint32_t issued = (1u << __shfl_sync(0xffffffffu, pre, 0)) - 1u;  // stages that were ever filled: bits
         bool ok = true;
         while (seg < sched.segs && ok) {
 #pragma unroll
@@ -816,10 +886,12 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                 if (seg < sched.segs && ok) {
                     const int stop = (kb | 1) + 1 < end ? (kb | 1) + 1 : end;
                     for (; kb < stop; ++kb) {
-                        ok = warp_wait_uniform(&bars.empty[s], par, p.wait_ns);
+                        ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
                         if (!ok)
                             break;
-                        if (group < 0 && lane == 0) {
+                        if (pre > 0) {
+                            --pre;
+                        } else if (group < 0 && lane == 0) {
                             if (rank == 0)
                                 mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
                             const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
@@ -849,7 +921,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                         }
                         if (++s == ST) {
                             s = 0;
-                            par ^= 1u;
+                            ++round;
                         }
                     }
                     if (kb >= end) {
@@ -862,15 +934,16 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         }
         // copies in flight end before the CTA does (the second CTA of a pair
         // leaves after the first, at the closing barrier).  Stages from s on
-        // were last filled in the round before this one.  If arrivals are
-        // missing, the limit that the first wait runs out of is long enough
-        // for all of them.
+        // were last filled in the round before this one (in round 0: early).
+        // If arrivals are missing, the limit that the first wait runs out of is
+        // long enough for all of them.
         if (group < 0 && rank == 0) {
             bool landed = true;
             for (int j = 0; j < ST && landed; ++j) {
                 const int st = s + j < ST ? s + j : s + j - ST;
+                const uint32_t filled = st < s || round == 0 ? round : round - 1;
                 if (issued >> st & 1u)
-                    landed = warp_wait_uniform(&bars.full[st], st >= s ? par : par ^ 1u, kDefaultWaitNs);
+                    landed = warp_wait_uniform(&bars.full[st], filled & 1u, kDefaultWaitNs);
             }
             ok = ok && landed;
         }
