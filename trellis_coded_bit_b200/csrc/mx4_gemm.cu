@@ -42,9 +42,10 @@
 namespace exl3 {
 
 constexpr int kMxBM = 128;                       // output channels per CTA's tile (TMEM lanes)
-constexpr int kMxBK = 256;                       // columns of k per unit: 128 bytes of codes
+constexpr int kMxBK = 512;                       // columns of k per unit: 16 scales of a row, two boxes of codes
+constexpr int kMxBoxK = 256;                     // columns of a box: 128 bytes of codes, the swizzle's width
 constexpr int kMxMmaWarp = 0, kMxFeedWarp0 = 1;  // then 1 + groups of 128 tokens feeding warps, then the epilogue
-constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 16 KB
+constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
 constexpr int kMxMaxExperts = 1024;
 constexpr size_t kMxSyncArea = 64 * 1024;
 constexpr int kMxSmemLimit = 232448 - 4 * (kMxMaxExperts + 1);  // what the tile table leaves
@@ -55,15 +56,15 @@ struct MxTile {
     static constexpr int kBRows = TN / CG;                      // token rows in this CTA's shared memory
     static constexpr int kBBytes = kBRows * kMxBK / 2;
     static constexpr int kBGroups = (TN + 127) / 128;           // 128-row groups of token scales
-    static constexpr int kScaleBytes = 1024 + kBGroups * 1024;  // two 128-column chunks of 512 bytes per group
+    static constexpr int kScaleBytes = 2048 + kBGroups * 2048;  // four 128-column chunks of 512 bytes per group
     static constexpr int kStageBytes = kMxABytes + kBBytes + kScaleBytes;
     static constexpr int kFeedWarps = 1 + kBGroups;             // one per 128 rows of scales
     static constexpr int kEpiWarp0 = kMxFeedWarp0 + kFeedWarps;
-    static constexpr int kDepth = 4;                            // 512-column steps of scales in flight
+    static constexpr int kDepth = 3;                            // units whose scales are loaded ahead
     static constexpr int kFit = (kMxSmemLimit - 2048) / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kAcc = TN > 128 ? 1 : 2;               // accumulators in TMEM
-    static constexpr int kScaleCols = 8 + 8 * kBGroups;         // TMEM columns of a stage's scales
+    static constexpr int kScaleCols = 16 + 16 * kBGroups;       // TMEM columns of a stage's scales
     static constexpr int kAccCols = TN < 32 ? 32 : TN;
     static constexpr int kEpiWarps = TN >= 128 ? 8 : 4;         // each: 32 lanes x kEpiCols columns
     static constexpr int kEpiCols = TN / (kEpiWarps / 4);
@@ -486,7 +487,6 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     if (lane == 0) {
         const uint64_t t0 = global_ns();
         while (!mbar_try_wait(&bars.acc_full[acc], par)) {
-            __nanosleep(100);
             if (global_ns() - t0 > p.wait_ns) {
                 ok = false;
                 break;
@@ -655,12 +655,14 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     const uint32_t worker = blockIdx.x / CG;
-    // Without experts the tiles are known at once, and the thread that issues
-    // the copies starts the first stages' weights before anything else: they do
-    // not depend on the kernel before (the tokens, and all else, wait for it).
+    // Without experts the tiles are known at once, and the warp that issues the
+    // copies waits for nobody: it sets up the barriers, begins the first stages
+    // and loads its first scales while the others set up.  What it reads before
+    // grid_dep_wait are weights alone.
     const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
+    const uint32_t tts = (uint32_t)((p.rows + TN - 1) / TN);  // without experts
     const bool early = CG == 1 && !p.offsets;
-    int pre = 0;  // stages begun early
+    const bool ahead = early && warp == kMxFeedWarp0;
     if (threadIdx.x == 32 * kMxFeedWarp0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&bars.full[s], 1 + CG * S::kFeedWarps);  // the bytes, each CTA's scales
@@ -673,76 +675,56 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         mbar_init(&bars.drain, 1);
         bars.epi_abort = 0;
         bars.ticket = 0;
-        fence_mbar_init();
         if (early) {
-            const uint32_t tts = (uint32_t)((p.rows + TN - 1) / TN);
             first[0] = 0;
             first[1] = nts * tts;
-            const MxSched sched = mx_schedule(nts * tts, (uint32_t)p.kb_count, gridDim.x / CG, worker);
-            int rows[ST], cols[ST];
-#pragma unroll
-            for (int seg = 0, kb = 0, end = 0, wrow = 0, xrow = 0; pre < ST; ++kb, ++pre) {
-                while (kb >= end && seg < sched.segs) {
-                    const MxSeg g = mx_seg(sched, seg++);
-                    kb = g.k0;
-                    end = g.k1;
-                    wrow = (int)(g.t / tts) * kMxBM;
-                    xrow = (int)(g.t % tts) * TN;
+        }
+        fence_mbar_init();
+    }
+    if (ahead) {
+        __syncwarp();
+        asm volatile("barrier.cta.arrive 2, %0;\n" ::"n"(S::kThreads) : "memory");
+    } else {
+        if (warp == kMxMmaWarp)
+            mx_tmem_alloc<CG>(&bars.tmem_slot);
+        grid_dep_wait();
+        grid_dep_launch();
+        if (warp == kMxMmaWarp && !early) {
+            // prefix sums of the experts' tiles
+            uint32_t run = 0;
+            for (int e0 = 0; e0 < p.experts; e0 += 32) {
+                uint32_t v = 0;
+                if (e0 + lane < p.experts) {
+                    int64_t lo, hi;
+                    mx_expert_rows(p, e0 + lane, lo, hi);
+                    v = (uint32_t)((hi - lo + TN - 1) / TN) * nts;
                 }
-                if (kb >= end)
-                    break;
-                mbar_arrive_expect_tx(&bars.full[pre], kMxABytes + S::kBBytes);
-                tma_load_2d<CG>(aring + pre * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, smem_addr(&bars.full[pre]));
-                rows[pre] = xrow;
-                cols[pre] = kb * (kMxBK / 2);
-            }
-            grid_dep_wait();
+                uint32_t incl = v;
 #pragma unroll
-            for (int s = 0; s < ST; ++s)
-                if (s < pre)
-                    tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, cols[s], rows[s], smem_addr(&bars.full[s]));
-        }
-    }
-    if (warp == kMxMmaWarp)
-        mx_tmem_alloc<CG>(&bars.tmem_slot);
-    grid_dep_wait();
-    grid_dep_launch();
-    if (warp == 0 && !early) {
-        // prefix sums of the experts' tiles
-        uint32_t run = 0;
-        for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            uint32_t v = 0;
-            if (e0 + lane < p.experts) {
-                int64_t lo, hi;
-                mx_expert_rows(p, e0 + lane, lo, hi);
-                v = (uint32_t)((hi - lo + TN - 1) / TN) * nts;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+                    incl += lane >= d ? o : 0;
+                }
+                if (e0 + lane < p.experts)
+                    first[e0 + lane] = run + incl - v;
+                run += __shfl_sync(0xffffffffu, incl, 31);
             }
-            uint32_t incl = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-                incl += lane >= d ? o : 0;
-            }
-            if (e0 + lane < p.experts)
-                first[e0 + lane] = run + incl - v;
-            run += __shfl_sync(0xffffffffu, incl, 31);
+            if (lane == 0)
+                first[p.experts] = run;
         }
-        if (lane == 0)
-            first[p.experts] = run;
+        tc_fence_before();
+        asm volatile("barrier.cta.sync 2, %0;\n" ::"n"(S::kThreads) : "memory");
+        if constexpr (CG == 2)
+            cluster_sync();  // the other CTA's barriers are ready
+        tc_fence_after();
     }
-    tc_fence_before();
-    __syncthreads();
-    if constexpr (CG == 2)
-        cluster_sync();  // the other CTA's barriers are ready
-    tc_fence_after();
-    const uint32_t tmem = bars.tmem_slot;
     const int KB = p.kb_count;
-    const MxSched sched = mx_schedule(first[p.experts], (uint32_t)KB, gridDim.x / CG, worker);
+    const MxSched sched = mx_schedule(early ? nts * tts : first[p.experts], (uint32_t)KB, gridDim.x / CG, worker);
 
     if (warp == kMxMmaWarp) {
         if (rank == 0 && sched.segs > 0) {
             // ------------------------------------------------ MMA issuer ---
-            const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t base = __shfl_sync(0xffffffffu, bars.tmem_slot, 0);
             const uint32_t a_base = __shfl_sync(0xffffffffu, smem_addr(aring), 0);
             const uint32_t b_base = a_base + ST * kMxABytes, s_base = b_base + ST * S::kBBytes;
             int s = 0;
@@ -762,39 +744,42 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                         break;
                     tc_fence_after();
                     const uint32_t tsa = base + (uint32_t)(S::kAcc * S::kAccCols + s * S::kScaleCols);
-                    const uint32_t tsb = tsa + 8;
+                    const uint32_t tsb = tsa + 16;
                     const uint32_t sc = s_base + (uint32_t)(s * S::kScaleBytes);
                     const uint64_t adesc = smem_desc(a_base + (uint32_t)(s * kMxABytes), 16, 1024);
                     const uint64_t bdesc = smem_desc(b_base + (uint32_t)(s * S::kBBytes), 16, 1024);
                     const int left = p.k - kb * kMxBK;
-                    const int steps = left >= kMxBK ? 4 : (left + 63) / 64;  // 64 columns per MMA; none behind k
+                    const int steps = left >= kMxBK ? 8 : (left + 63) / 64;  // 64 columns per MMA; none behind k
                     uint64_t *const done = &bars.empty[s];
                     if (elect_one()) {
                         // chunk c's scales: weights at tsa + 4c, tokens at tsb + 4 groups c
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             tmem_copy_scales<CG>(tsa + 4 * c, sc + 512 * c);
 #pragma unroll
                             for (int h = 0; h < S::kBGroups; ++h)
                                 tmem_copy_scales<CG>(tsb + 4 * (c * S::kBGroups + h),
-                                                     sc + 1024 + 512 * (c * S::kBGroups + h));
+                                                     sc + 2048 + 512 * (c * S::kBGroups + h));
                         }
-                        // 64 columns are 32 bytes: 2 in the descriptors' address field
+                        // 64 columns are 32 bytes: 2 in the descriptors' address
+                        // field; the second box lies behind the first
                         auto mma = [&](int j, uint32_t add) {
-                            mma_mxf4<CG>(d, adesc + 2 * j, bdesc + 2 * j,
+                            const uint64_t at = 2 * (j & 3);
+                            mma_mxf4<CG>(d, adesc + at + (j >> 2) * (kMxABytes / 2 / 16),
+                                         bdesc + at + (j >> 2) * (S::kBBytes / 2 / 16),
                                          (j & 1) ? mx_idesc<TN, CG>(1) : mx_idesc<TN, CG>(0), tsa + 4 * (j >> 1),
                                          tsb + 4 * S::kBGroups * (j >> 1), add);
                         };
                         mma(0, kb > g.k0 ? 1u : 0u);
-                        if (steps == 4) {
-                            mma(1, 1u);
-                            mma(2, 1u);
-                            mma(3, 1u);
+                        if (steps == 8) {
+#pragma unroll
+                            for (int j = 1; j < 8; ++j)
+                                mma(j, 1u);
                         } else {
-                            if (steps > 1)
-                                mma(1, 1u);
-                            if (steps > 2)
-                                mma(2, 1u);
+#pragma unroll
+                            for (int j = 1; j < 7; ++j)
+                                if (j < steps)
+                                    mma(j, 1u);
                         }
                         mx_commit<CG>(done);
                         if (kb + 1 == g.k1)
@@ -823,8 +808,8 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         // the 128 weight rows, the others those of 128 token rows each.  Lane
         // l owns rows l, l + 32, l + 64, l + 96, whose scales of 128 columns
         // are the 16 bytes at 16 l of the layout that the tensor core wants:
-        // one conflict-free store.  It loads 16 scales of each row (512
-        // columns, a step) kDepth steps ahead into registers.
+        // one conflict-free store.  It loads a unit's 16 scales of each row
+        // kDepth units ahead into registers.
         const int group = warp - kMxFeedWarp0 - 1;  // -1: weights
         const int kblocks = p.k / kMx4Block;
         // load side: segment, unit and rows of the next step
@@ -848,13 +833,12 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         auto fetch = [&](uint4 (&q)[4]) {
             if (fseg >= sched.segs)
                 return;
-            const uint8_t *src = from + (int64_t)(fkb >> 1) * 16;
+            const uint8_t *src = from + (int64_t)fkb * 16;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 q[j] = 32 * j < have && 32 * j + lane < most ? *reinterpret_cast<const uint4 *>(src + (int64_t)(32 * j) * p.stride)
                                                              : make_uint4(0u, 0u, 0u, 0u);
-            fkb = (fkb | 1) + 1;  // the step serves the pair's units up to the segment's end
-            if (fkb >= fend) {
+            if (++fkb == fend) {
                 ++fseg;
                 enter();
             }
@@ -877,40 +861,80 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             }
         };
         next();
+        int pre = 0;  // stages begun below
+        if (ahead) {
+            // lane l begins stage l with this worker's unit l
+            int seg0 = 0, unit = lane;
+            while (seg0 < sched.segs) {
+                const MxSeg g = mx_seg(sched, seg0);
+                if (unit < g.k1 - g.k0)
+                    break;
+                unit -= g.k1 - g.k0;
+                ++seg0;
+            }
+            const bool mine = lane < ST && seg0 < sched.segs;
+            int col = 0, row = 0;
+            if (mine) {
+                const MxSeg g = mx_seg(sched, seg0);
+                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                col = (g.k0 + unit) * (kMxBK / 2);
+                row = (int)w.row;
+                mbar_arrive_expect_tx(&bars.full[lane], kMxABytes + S::kBBytes);
+                for (int h = 0; h < 2; ++h)
+                    tma_load_2d<CG>(aring + lane * kMxABytes + h * (kMxABytes / 2), &wmap, col + h * (kMxBoxK / 2),
+                                    (int)w.wrow, smem_addr(&bars.full[lane]));
+            }
+            pre = __popc(__ballot_sync(0xffffffffu, mine));
+            grid_dep_wait();
+            grid_dep_launch();
+            if (mine)
+                for (int h = 0; h < 2; ++h)
+                    tma_load_2d<CG>(bring + lane * S::kBBytes + h * (S::kBBytes / 2), &xmap, col + h * (kMxBoxK / 2), row,
+                                    smem_addr(&bars.full[lane]));
+        }
         uint32_t round = 0;  // of the ring
-        uint32_t issued = (1u << __shfl_sync(0xffffffffu, pre, 0)) - 1u;  // stages that were ever filled: bits
+        uint32_t issued = (1u << pre) - 1u;  // stages that were ever filled: bits
         bool ok = true;
         while (seg < sched.segs && ok) {
 #pragma unroll
             for (int d = 0; d < S::kDepth; ++d) {
                 if (seg < sched.segs && ok) {
-                    const int stop = (kb | 1) + 1 < end ? (kb | 1) + 1 : end;
-                    for (; kb < stop; ++kb) {
-                        ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
-                        if (!ok)
-                            break;
+                    ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
+                    if (ok) {
                         if (pre > 0) {
                             --pre;
-                        } else if (group < 0 && lane == 0) {
-                            if (rank == 0)
-                                mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
+                        } else if (group < 0) {
                             const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
-                            tma_load_2d<CG>(aring + s * kMxABytes, &wmap, kb * (kMxBK / 2), wrow, bar);
-                            tma_load_2d<CG>(bring + s * S::kBBytes, &xmap, kb * (kMxBK / 2), xrow, bar);
+                            if (elect_one()) {
+                                if (rank == 0)
+                                    mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
+                                    tma_load_2d<CG>(aring + s * kMxABytes + h * (kMxABytes / 2), &wmap, col, wrow, bar);
+                                    tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
+                                }
+                            }
+                            __syncwarp();
                         }
                         issued |= 1u << s;
-                        unsigned char *sc = scales + s * S::kScaleBytes + lane * 16 + (group < 0 ? 0 : 1024 + 512 * group);
+                        unsigned char *sc = scales + s * S::kScaleBytes + lane * 16 + (group < 0 ? 0 : 2048 + 512 * group);
+                        const int step = group < 0 ? 512 : 512 * S::kBGroups;
                         const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
-                        const uint32_t m0 = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
-                        const uint32_t m1 = left >= 8 ? 0xffffffffu : (left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u);
+                        uint32_t keep[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int n4 = left - 4 * c;
+                            keep[c] = n4 >= 4 ? 0xffffffffu : (n4 <= 0 ? 0u : (1u << (8 * n4)) - 1u);
+                        }
                         const uint4 *v = q[d];
-                        const bool odd = kb & 1;
-                        *reinterpret_cast<uint4 *>(sc) =
-                            make_uint4((odd ? v[0].z : v[0].x) & m0, (odd ? v[1].z : v[1].x) & m0,
-                                       (odd ? v[2].z : v[2].x) & m0, (odd ? v[3].z : v[3].x) & m0);
-                        *reinterpret_cast<uint4 *>(sc + (group < 0 ? 512 : 512 * S::kBGroups)) =
-                            make_uint4((odd ? v[0].w : v[0].y) & m1, (odd ? v[1].w : v[1].y) & m1,
-                                       (odd ? v[2].w : v[2].y) & m1, (odd ? v[3].w : v[3].y) & m1);
+                        *reinterpret_cast<uint4 *>(sc) = make_uint4(v[0].x & keep[0], v[1].x & keep[0], v[2].x & keep[0], v[3].x & keep[0]);
+                        *reinterpret_cast<uint4 *>(sc + step) =
+                            make_uint4(v[0].y & keep[1], v[1].y & keep[1], v[2].y & keep[1], v[3].y & keep[1]);
+                        *reinterpret_cast<uint4 *>(sc + 2 * step) =
+                            make_uint4(v[0].z & keep[2], v[1].z & keep[2], v[2].z & keep[2], v[3].z & keep[2]);
+                        *reinterpret_cast<uint4 *>(sc + 3 * step) =
+                            make_uint4(v[0].w & keep[3], v[1].w & keep[3], v[2].w & keep[3], v[3].w & keep[3]);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -923,10 +947,10 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                             s = 0;
                             ++round;
                         }
-                    }
-                    if (kb >= end) {
-                        ++seg;
-                        next();
+                        if (++kb == end) {
+                            ++seg;
+                            next();
+                        }
                     }
                     fetch(q[d]);
                 }
@@ -952,7 +976,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     } else {
         // ---------------------------------------------------- epilogue ---
         for (int seg = 0; seg < sched.segs; ++seg)
-            if (!mx_epilogue<T, TN, CG>(p, bars, first, sched, tmem, seg, rank))
+            if (!mx_epilogue<T, TN, CG>(p, bars, first, sched, bars.tmem_slot, seg, rank))
                 break;
     }
 
@@ -962,7 +986,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         cluster_sync();  // the other CTA's commits and arrivals have landed, its MMAs are done
     if (warp == kMxMmaWarp) {
         tc_fence_after();
-        mx_tmem_dealloc<CG>(tmem);
+        mx_tmem_dealloc<CG>(bars.tmem_slot);
     }
 }
 
@@ -998,7 +1022,7 @@ static bool code_map(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t boxes[2] = {128, (cuuint32_t)box};
+    const cuuint32_t boxes[2] = {kMxBoxK / 2, (cuuint32_t)box};
     const cuuint32_t steps[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)codes, dims, strides, boxes, steps,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
