@@ -167,6 +167,21 @@ def test_dequantize_every_code_and_scale():
         assert torch.equal(torch.nan_to_num(out.float(), nan=77.0), torch.nan_to_num(ref.to(dtype).float(), nan=77.0))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dequantize_onto_16_byte_alignment(dtype):
+    """An output that starts on 16 bytes but not on 32."""
+    rng = np.random.default_rng(6)
+    c, s = operand(rng, 5, 96, 100, 140)
+    pc, ps = (dev(a) for a in mx4.pack(c, s))
+    skip = 16 // torch.empty((), dtype=dtype).element_size()
+    buf = torch.zeros(5 * 96 + 2 * skip, dtype=dtype, device="cuda")
+    out = buf[skip:skip + 5 * 96].view(5, 96)
+    assert out.data_ptr() % 32 == 16
+    exl3.exl3_mx4_dequantize(pc, ps, out=out)
+    assert torch.equal(out.cpu(), torch.from_numpy(mx4.values(c, s)).to(dtype))
+    assert not buf[:skip].any() and not buf[-skip:].any()
+
+
 # ----------------------------------------------------------------- product ---
 
 def operand(rng, rows, k, low=127, high=127):

@@ -36,6 +36,20 @@ __device__ __forceinline__ void load8(const T *p, float (&v)[8])
     }
 }
 
+// Row and column group of group g of a matrix with `groups` a row (64-bit
+// division costs ten times the 32-bit one, which nearly every matrix allows).
+__device__ __forceinline__ void split_group(int64_t g, int groups, int64_t &row, int &c)
+{
+    if ((uint64_t)g >> 32) {
+        row = g / groups;
+        c = (int)(g - row * groups);
+    } else {
+        const uint32_t r = (uint32_t)g / (uint32_t)groups;
+        row = r;
+        c = (int)((uint32_t)g - r * (uint32_t)groups);
+    }
+}
+
 // Codes of 8 scaled values, the first in the lowest 4 bits (round to nearest
 // even, saturating).
 __device__ __forceinline__ uint32_t codes8(const float (&r)[8])
@@ -147,8 +161,10 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams 
     for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x - (threadIdx.x & 31); g0 < total; g0 += stride) {
         const int64_t g = g0 + (threadIdx.x & 31);
         const bool live = g < total;
-        const int64_t row = live ? g / groups : 0;
-        const int c = live ? (int)(g - row * groups) : 0;
+        int64_t row = 0;
+        int c = 0;
+        if (live)
+            split_group(g, groups, row, c);
         float v[8];
         load8<T>((const T *)p.x + (row * groups + c) * 8, v);
         if (p.signs) {
@@ -191,12 +207,10 @@ __device__ __forceinline__ void rotate32x4(F (&v)[32])
             }
 #pragma unroll
     for (int m = 1; m < 4; m <<= 1) {
-        const bool upper = (threadIdx.x & m) != 0;
+        const F sign = (threadIdx.x & m) ? F(-1) : F(1);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const F o = __shfl_xor_sync(0xffffffffu, v[i], m);
-            v[i] = upper ? o - v[i] : v[i] + o;
-        }
+        for (int i = 0; i < 32; ++i)
+            v[i] = fma(sign, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));  // v + o, or o - v
     }
 }
 
@@ -268,7 +282,7 @@ __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *sign
 // factor 1/sqrt(128) 2^-e and the product with it are off by 2^-24 of a result
 // below 8 each: 2^-20.  Together, in units of the scale,
 //     |r - exact| <= 2^-21 S 2^-e / sqrt(128) + 2^-20,
-// of which `slack` is twice the first part, for the roundings of S and slack.
+// and `slack` is 2^-8 more than that, for the roundings of S and of itself.
 template <typename T>
 __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4QuantParams p)
 {
@@ -279,8 +293,10 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
     for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x - (threadIdx.x & 31); g0 < total; g0 += stride) {
         const int64_t g = g0 + (threadIdx.x & 31);
         const bool live = g < total;
-        const int64_t row = live ? g / p.blocks : 0;
-        const int c = live ? (int)(g - row * p.blocks) : (int)(threadIdx.x & 3);
+        int64_t row = 0;
+        int c = (int)(threadIdx.x & 3);
+        if (live)
+            split_group(g, p.blocks, row, c);
         const T *const x = (const T *)p.x + (row * p.blocks + c) * 32;
         const __half *const signs = p.signs ? p.signs + c * 32 : nullptr;
         float v[32];
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
         bool sure = sum == 0.f;
         if (!sure && byte >= 1 && byte <= 253 && sum < 1e38f) {
             const float inv = inverse_scale32(byte) * s;
-            const float slack = fmaf(0x1p-20f * sum, inv, 0x1p-20f);
+            const float slack = fmaf(0x1.01p-21f * sum, inv, 0x1.01p-20f);
             const float most = top * inv;
             uint32_t out[4], differ = 0;
 #pragma unroll
@@ -325,12 +341,12 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
                 float lo[8], hi[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float r = v[8 * i + j] * inv;
-                    lo[j] = r - slack;
-                    hi[j] = r + slack;
+                    lo[j] = fmaf(v[8 * i + j], inv, -slack);
+                    hi[j] = fmaf(v[8 * i + j], inv, slack);
                 }
-                out[i] = unsigned_zeros(codes8(lo));
-                differ |= out[i] ^ unsigned_zeros(codes8(hi));
+                const uint32_t a = codes8(lo);
+                differ |= (a ^ codes8(hi)) & 0x77777777u;  // equal magnitudes above 0 have equal signs
+                out[i] = unsigned_zeros(a);
             }
             code = make_uint4(out[0], out[1], out[2], out[3]);
             sure = differ == 0 && most > 4.f + slack && most < 8.f - slack;
@@ -348,35 +364,67 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
 
 // ------------------------------------------------------------ dequantise ---
 
+// 8 fp32 values in one 32-byte store.
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+constexpr int kDequantAhead = 4;  // groups of 8 values whose loads a thread keeps in flight
+
+// Bound by the values' bytes.  A thread writes 8 consecutive values (16 or 32
+// bytes) of each of 4 groups that lie a grid apart; `wide`: fp32 rows start on
+// 32 bytes, as the 32-byte store needs.
 template <typename T>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *__restrict__ codes,
                                                              const uint8_t *__restrict__ scales, int64_t rows,
-                                                             int groups, int stride, T *__restrict__ w)
+                                                             int groups, int stride, bool wide, T *__restrict__ w)
 {
     grid_dep_wait();
     grid_dep_launch();
     const int64_t total = rows * groups;
-    for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < total; g += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = g / groups;
-        const int c = (int)(g - row * groups);
-        const uint32_t code = codes[g];
-        const int b = scales[row * stride + (c >> 2)];
-        const float s = b == 255 ? __uint_as_float(0x7fc00000u)
-                                 : (b ? __uint_as_float((uint32_t)b << 23) : __uint_as_float(0x00400000u));
-        float v[8];
+    const int64_t threads = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g0 < total; g0 += threads * kDequantAhead) {
+        uint32_t code[kDequantAhead];
+        int byte[kDequantAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t q = (code >> (4 * i)) & 15u;
-            // exponent 0: mantissa/2; else (1 + mantissa/2) 2^(exponent - 1)
-            const uint32_t ex = (q >> 1) & 3u, man = q & 1u;
-            const float mag = ex ? __uint_as_float(((126u + ex) << 23) | (man << 22)) : 0.5f * (float)man;
-            v[i] = ((q & 8u) ? -mag : mag) * s;
+        for (int j = 0; j < kDequantAhead; ++j) {
+            const int64_t g = g0 + j * threads;
+            if (g < total) {
+                int64_t row;
+                int c;
+                split_group(g, groups, row, c);
+                code[j] = codes[g];
+                byte[j] = scales[row * stride + (c >> 2)];
+            }
         }
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(w + g * 8) = pack16<T>(v);
-        } else {
-            *reinterpret_cast<float4 *>(w + g * 8) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(w + g * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int j = 0; j < kDequantAhead; ++j) {
+            const int64_t g = g0 + j * threads;
+            if (g >= total)
+                break;
+            const int b = byte[j];
+            const float s = b == 255 ? __uint_as_float(0x7fc00000u)
+                                     : (b ? __uint_as_float((uint32_t)b << 23) : __uint_as_float(0x00400000u));
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t q = (code[j] >> (4 * i)) & 15u;
+                // exponent 0: mantissa/2; else (1 + mantissa/2) 2^(exponent - 1)
+                const uint32_t ex = (q >> 1) & 3u, man = q & 1u;
+                const float mag = ex ? __uint_as_float(((126u + ex) << 23) | (man << 22)) : 0.5f * (float)man;
+                v[i] = ((q & 8u) ? -mag : mag) * s;
+            }
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4 *>(w + g * 8) = pack16<T>(v);
+            } else if (wide) {
+                store8(w + g * 8, v);
+            } else {
+                *reinterpret_cast<float4 *>(w + g * 8) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(w + g * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
         }
     }
 }
@@ -464,20 +512,21 @@ extern "C" exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *
         ranges_overlap(scales, (size_t)(rows * mx4_scale_stride(k)), w, wb))
         return EXL3_ERR_INVALID_ARG;
     const int groups = (int)(k / 8), stride = (int)mx4_scale_stride(k);
-    const dim3 grid(mx4_grid(rows * groups, 256)), block(256);
+    const dim3 grid(mx4_grid((rows * groups + kDequantAhead - 1) / kDequantAhead, 256)), block(256);
+    const bool wide = ((uintptr_t)w & 31u) == 0;
     cudaStream_t s = (cudaStream_t)stream;
     const uint32_t *c = (const uint32_t *)codes;
     cudaError_t e;
     switch (dtype) {
     case EXL3_F16:
-        e = launch_kernel(mx4_dequantize_kernel<__half>, grid, block, 0, s, c, scales, rows, groups, stride, (__half *)w);
+        e = launch_kernel(mx4_dequantize_kernel<__half>, grid, block, 0, s, c, scales, rows, groups, stride, wide, (__half *)w);
         break;
     case EXL3_BF16:
         e = launch_kernel(mx4_dequantize_kernel<__nv_bfloat16>, grid, block, 0, s, c, scales, rows, groups, stride,
-                          (__nv_bfloat16 *)w);
+                          wide, (__nv_bfloat16 *)w);
         break;
     default:
-        e = launch_kernel(mx4_dequantize_kernel<float>, grid, block, 0, s, c, scales, rows, groups, stride, (float *)w);
+        e = launch_kernel(mx4_dequantize_kernel<float>, grid, block, 0, s, c, scales, rows, groups, stride, wide, (float *)w);
     }
     return e == cudaSuccess ? launch_status() : EXL3_ERR_CUDA;
 }

@@ -417,11 +417,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
 // bytes of a token's 32 channels (`wide`: y's rows are 16-byte aligned).
 // Otherwise each lane stores its own channel 8 times.  yt: y at the first token
 // and the warp's first channel; ch_left: channels of y from there on.
-template <typename T>
+// FULL: 8 tokens and 32 channels exist and rows are aligned; without branches
+// the exchanges of several calls overlap.
+template <typename T, bool FULL = false>
 __device__ __forceinline__ void mx_store8(T *yt, int64_t n, const uint32_t *v, int tokens, int ch_left, bool wide)
 {
     const int lane = threadIdx.x & 31;
-    if (wide) {
+    if (FULL || wide) {
         // lanes 1 apart: register i becomes (channel pair, token 2i + (lane & 1))
         const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
         uint32_t a[4], c[4], e[4];
@@ -449,7 +451,7 @@ __device__ __forceinline__ void mx_store8(T *yt, int64_t n, const uint32_t *v, i
             e[2 + h] = b2 ? c[2 + h] : got;
         }
         const int token = lane & 7, group = lane & 24;
-        if (token < tokens && group < ch_left)
+        if (FULL || (token < tokens && group < ch_left))
             *reinterpret_cast<uint4 *>(yt + token * n + group) = make_uint4(e[0], e[1], e[2], e[3]);
     } else if (lane < ch_left) {
         uint16_t *q = reinterpret_cast<uint16_t *>(yt + lane);
@@ -519,13 +521,24 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
         // everything into registers (16 bits each), so that the MMA issuer
         // gets the accumulator back before the stores
         uint32_t v[kCols / 2];
+        if constexpr (kCols % 32 == 0) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-            uint32_t b[16];
-            EXL3_TMEM_LD16(d + c, b);
+            for (int c = 0; c < kCols; c += 32) {
+                uint32_t b[32];
+                EXL3_TMEM_LD32(d + c, b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[c / 2 + i] = pack2<T>(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+                for (int i = 0; i < 16; ++i)
+                    v[c / 2 + i] = pack2<T>(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+                uint32_t b[16];
+                EXL3_TMEM_LD16(d + c, b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[c / 2 + i] = pack2<T>(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+            }
         }
         tc_fence_before();
         __syncwarp();
@@ -534,6 +547,12 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                 mbar_arrive(&bars.acc_empty[acc]);
             else
                 mbar_arrive_leader(&bars.acc_empty[acc]);
+        }
+        if (wide && cols == kCols && ch_left >= 32) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8)
+                mx_store8<T, true>(y + (int64_t)c * p.n, p.n, v + c / 2, 8, 32, true);
+            return true;
         }
 #pragma unroll
         for (int c = 0; c < kCols; c += 8)

@@ -532,11 +532,11 @@ def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None
     if signs is not None:
         _shape(signs, (k,), "signs")
     if codes is None:
-        codes = torch.empty((to, k // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((to, k // 2), dtype=torch.uint8)
     else:
         _shape(codes, (to, k // 2), "codes")
     if scales is None:
-        scales = torch.empty((to, stride), dtype=torch.uint8, device=x.device)
+        scales = x.new_empty((to, stride), dtype=torch.uint8)
     else:
         _shape(scales, (to, stride), "scales")
     _call("exl3_mx4_quantize", device, stream, _arg(x, x.dtype, "x", device), dtype,
@@ -550,7 +550,7 @@ def exl3_mx4_dequantize(codes, scales, dtype=torch.float16, out=None, stream=Non
     """The values of a 4-bit matrix, rows x k, as fp16, bf16 or fp32."""
     (rows,), k = _mx4_operand(codes, scales, 1, "matrix")
     if out is None:
-        out = torch.empty((rows, k), dtype=dtype, device=codes.device)
+        out = codes.new_empty((rows, k), dtype=dtype)
     else:
         _shape(out, (rows, k), "out")
     device, dt = _device(out, "out", DTYPES)
@@ -570,7 +570,7 @@ def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None,
     if kw != k:
         raise ValueError("x has k = %d, w has %d" % (k, kw))
     if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=xc.device)
+        y = xc.new_empty((m, n), dtype=dtype)
     else:
         _shape(y, (m, n), "y")
     device, dt = _device(y, "y", _HALF_TYPES)
@@ -598,7 +598,7 @@ def exl3_mx4_linear(x, wc, ws, signs=None, rotate=False, y=None, workspace=None,
     if signs is not None:
         _shape(signs, (k,), "signs")
     if y is None:
-        y = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        y = x.new_empty((m, n), dtype=x.dtype)
     else:
         _shape(y, (m, n), "y")
     _call("exl3_mx4_linear", device, stream, _arg(x, x.dtype, "x", device), dt,
@@ -621,7 +621,7 @@ def exl3_mx4_matmul_experts(xc, xs, offsets, wc, ws, dtype=torch.float16, y=None
         raise ValueError("x has k = %d, w has %d" % (k, kw))
     _shape(offsets, (experts + 1,), "offsets")
     if y is None:
-        y = torch.empty((rows, n), dtype=dtype, device=xc.device)
+        y = xc.new_empty((rows, n), dtype=dtype)
     else:
         _shape(y, (rows, n), "y")
     device, dt = _device(y, "y", _HALF_TYPES)
@@ -645,11 +645,11 @@ def exl3_moe_sort(ids, experts, offsets=None, positions=None, workspace=None, st
     tokens, topk = ids.shape
     device, _ = _device(ids, "ids", (torch.int32,))
     if offsets is None:
-        offsets = torch.empty((experts + 1,), dtype=torch.int32, device=ids.device)
+        offsets = ids.new_empty((experts + 1,), dtype=torch.int32)
     else:
         _shape(offsets, (experts + 1,), "offsets")
     if positions is None:
-        positions = torch.empty((tokens, topk), dtype=torch.int32, device=ids.device)
+        positions = ids.new_empty((tokens, topk), dtype=torch.int32)
     else:
         _shape(positions, (tokens, topk), "positions")
     _call("exl3_moe_sort", device, stream, _arg(ids, torch.int32, "ids", device), tokens, topk, experts,
@@ -693,7 +693,7 @@ def exl3_moe_combine(ys, positions, weights=None, y=None, stream=None):
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
     if y is None:
-        y = torch.empty((tokens, h), dtype=ys.dtype, device=ys.device)
+        y = ys.new_empty((tokens, h), dtype=ys.dtype)
     else:
         _shape(y, (tokens, h), "y")
     _call("exl3_moe_combine", device, stream, _arg(ys, ys.dtype, "ys", device), dt,
@@ -715,11 +715,11 @@ def exl3_moe_combine_grad(dy, ys, positions, weights=None, dys=None, dweights=No
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
     if dys is None:
-        dys = torch.empty((rows, h), dtype=dy.dtype, device=dy.device)
+        dys = dy.new_empty((rows, h), dtype=dy.dtype)
     else:
         _shape(dys, (rows, h), "dys")
     if dweights is None:
-        dweights = torch.empty((tokens, topk), dtype=torch.float32, device=dy.device)
+        dweights = dy.new_empty((tokens, topk), dtype=torch.float32)
     else:
         _shape(dweights, (tokens, topk), "dweights")
     _call("exl3_moe_combine_grad", device, stream, _arg(dy, dy.dtype, "dy", device),
