@@ -188,9 +188,14 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams 
 
 // ------------------------------------------------------ with the rotation ---
 //
-// A thread takes a block of 32 columns (no exchange for its largest magnitude,
-// one 16-byte store of codes), 4 lanes the 128 of a rotation: five butterfly
-// stages in registers, two across lanes.
+// 4 lanes take the 128 columns of a rotation and end with a block of 32 each (no
+// exchange for its largest magnitude, one 16-byte store of codes).  Lane l loads
+// columns 32 p + 8 l .. + 7 of the four blocks p, so that 4 lanes read 64
+// contiguous bytes; five butterfly stages run over what a lane holds (the low 3
+// and high 2 bits of the column), then the lanes exchange halves so that block
+// p = l is theirs, and the two stages of the middle bits follow in registers.
+// That is 32 shuffles; with a block per lane from the start the same two stages
+// took 64, the loads touched four times the lines, and both share one pipe.
 
 // 32-point Sylvester Hadamard in registers, then over the lanes 1 and 2 apart.
 template <typename F>
@@ -212,6 +217,83 @@ __device__ __forceinline__ void rotate32x4(F (&v)[32])
         for (int i = 0; i < 32; ++i)
             v[i] = fma(sign, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));  // v + o, or o - v
     }
+}
+
+// fp32 arithmetic on two values an instruction.
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 f2(float a, float b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack(F2 p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// The rotation of the 128 columns of 4 lanes: v[4p + r/2] holds columns
+// 32p + 8l + r, r + 1 before, block l's columns 8p + r, r + 1 after.
+__device__ __forceinline__ void rotate32x4(F2 (&v)[16])
+{
+    const F2 minus = f2(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float a, b;
+        unpack(v[i], a, b);
+        v[i] = f2(a + b, a - b);
+    }
+#pragma unroll
+    for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i & h) == 0) {
+                const F2 a = v[i], b = v[i + h];
+                v[i] = add2(a, b);
+                v[i + h] = fma2(b, minus, a);
+            }
+    // lane bit m <-> bit 4m of i: keep the half whose bit equals the lane's
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const bool upper = (threadIdx.x & m) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i & (4 * m)) == 0) {
+                F2 &lo = v[i], &hi = v[i + 4 * m];
+                float a, b;
+                unpack(upper ? lo : hi, a, b);
+                const F2 got = f2(__shfl_xor_sync(0xffffffffu, a, m), __shfl_xor_sync(0xffffffffu, b, m));
+                lo = upper ? got : lo;
+                hi = upper ? hi : got;
+            }
+    }
+#pragma unroll
+    for (int h = 4; h < 16; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i & h) == 0) {
+                const F2 a = v[i], b = v[i + h];
+                v[i] = add2(a, b);
+                v[i + h] = fma2(b, minus, a);
+            }
 }
 
 // Codes of zero magnitude without their sign.
@@ -276,6 +358,71 @@ __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *sign
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// Columns 32 p + 8 l .. + 7, p = 0 .. 3, of the 128 from x (x and signs: at column
+// 8 l) times their signs.  Signs of exactly +-1 (the usual ones) flip the
+// sign bits of 16-bit values in place, a third of the instructions of
+// converting and multiplying them.
+template <typename T>
+__device__ __forceinline__ void load_signed(const T *x, const __half *signs, F2 (&v)[16])
+{
+    if constexpr (sizeof(T) == 2) {
+        uint4 raw[4], sg[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw[i] = *reinterpret_cast<const uint4 *>(x + 32 * i);
+        if (signs) {
+            uint32_t other = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sg[i] = *reinterpret_cast<const uint4 *>(signs + 32 * i);
+                other |= ((sg[i].x ^ 0x3c003c00u) | (sg[i].y ^ 0x3c003c00u) | (sg[i].z ^ 0x3c003c00u) | (sg[i].w ^ 0x3c003c00u)) &
+                         0x7fff7fffu;
+            }
+            if (other == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    raw[i].x ^= sg[i].x & 0x80008000u;
+                    raw[i].y ^= sg[i].y & 0x80008000u;
+                    raw[i].z ^= sg[i].z & 0x80008000u;
+                    raw[i].w ^= sg[i].w & 0x80008000u;
+                }
+                signs = nullptr;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[8];
+            unpack16<T>(raw[i], f);
+            if (signs) {
+                float s[8];
+                unpack16<__half>(sg[i], s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] *= s[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[4 * i + j] = f2(f[2 * j], f[2 * j + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[8];
+            load8<T>(x + 32 * i, f);
+            if (signs) {
+                float s[8];
+                load8<__half>(signs + 32 * i, s);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] *= s[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[4 * i + j] = f2(f[2 * j], f[2 * j + 1]);
+        }
+    }
+}
+
 // Error bound.  Each of the 7 stages rounds values whose magnitudes, over the
 // tree of one output, add up to at most S = sum |x .* signs| (128 values), by
 // 2^-24 each: 7 2^-24 S, and 2^-24 S for the products with the signs.  The
@@ -299,33 +446,25 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
             split_group(g, p.blocks, row, c);
         const T *const x = (const T *)p.x + (row * p.blocks + c) * 32;
         const __half *const signs = p.signs ? p.signs + c * 32 : nullptr;
-        float v[32];
+        F2 v[16];
+        const int shift = 24 * (int)(threadIdx.x & 3);  // from column 32 l to column 8 l
+        load_signed(x - shift, signs ? signs - shift : nullptr, v);
+        float sum = 0.f, top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            float f[8];
-            load8<T>(x + i, f);
-            if (signs) {
-                float s[8];
-                load8<__half>(signs + i, s);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[j] *= s[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i + j] = f[j];
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack(v[i], a, b);
+            sum += fabsf(a) + fabsf(b);
         }
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            sum += fabsf(v[i]);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         rotate32x4(v);
-        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            top = fmaxf(top, fabsf(v[i]));
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack(v[i], a, b);
+            top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+        }
         const float s = 0.08838834764831845f;  // 1/sqrt(128)
         int byte = scale_byte32(__float_as_uint(top * s));
         uint4 code = make_uint4(0u, 0u, 0u, 0u);
@@ -335,14 +474,15 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
             const float inv = inverse_scale32(byte) * s;
             const float slack = fmaf(0x1.01p-21f * sum, inv, 0x1.01p-20f);
             const float most = top * inv;
+            const F2 inv2 = f2(inv, inv);
             uint32_t out[4], differ = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float lo[8], hi[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    lo[j] = fmaf(v[8 * i + j], inv, -slack);
-                    hi[j] = fmaf(v[8 * i + j], inv, slack);
+                for (int j = 0; j < 4; ++j) {
+                    unpack(fma2(v[4 * i + j], inv2, f2(-slack, -slack)), lo[2 * j], lo[2 * j + 1]);
+                    unpack(fma2(v[4 * i + j], inv2, f2(slack, slack)), hi[2 * j], hi[2 * j + 1]);
                 }
                 const uint32_t a = codes8(lo);
                 differ |= (a ^ codes8(hi)) & 0x77777777u;  // equal magnitudes above 0 have equal signs
@@ -363,6 +503,28 @@ __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4Quant
 }
 
 // ------------------------------------------------------------ dequantise ---
+
+// Magnitudes and signs of 8 codes (exact in fp16, through which the conversion goes).
+__device__ __forceinline__ void decode8(uint32_t code, float (&v)[8])
+{
+    uint32_t h[4];
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(code));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __half2 p;
+        memcpy(&p, &h[i], 4);
+        const float2 f = __half22float2(p);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
 
 // 8 fp32 values in one 32-byte store.
 __device__ __forceinline__ void store8(float *p, const float (&v)[8])
@@ -409,14 +571,10 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t *__r
             const float s = b == 255 ? __uint_as_float(0x7fc00000u)
                                      : (b ? __uint_as_float((uint32_t)b << 23) : __uint_as_float(0x00400000u));
             float v[8];
+            decode8(code[j], v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t q = (code[j] >> (4 * i)) & 15u;
-                // exponent 0: mantissa/2; else (1 + mantissa/2) 2^(exponent - 1)
-                const uint32_t ex = (q >> 1) & 3u, man = q & 1u;
-                const float mag = ex ? __uint_as_float(((126u + ex) << 23) | (man << 22)) : 0.5f * (float)man;
-                v[i] = ((q & 8u) ? -mag : mag) * s;
-            }
+            for (int i = 0; i < 8; ++i)
+                v[i] *= s;
             if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<uint4 *>(w + g * 8) = pack16<T>(v);
             } else if (wide) {
