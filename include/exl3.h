@@ -421,7 +421,7 @@ exl3_status exl3_mx4_linear(const void *x, int dtype, const void *signs, int rot
  *            values outside [0, rows] are taken to its ends.
  *   xc, xs   rows x k; wc, ws  experts x n x k; y  rows x n fp16 or bf16.
  *            Rows of y from offsets[experts] on keep what they hold.
- *   experts  1 .. 1024 (experts * n <= 2^30).
+ *   experts  1 .. 512 (experts * n <= 2^30).
  * Otherwise as exl3_mx4_matmul.
  */
 size_t exl3_mx4_matmul_experts_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts);

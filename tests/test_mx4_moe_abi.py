@@ -79,7 +79,7 @@ def test_matmul_workspace():
     assert exl3.exl3_mx4_matmul_workspace_size(4, 100, 64) == 0
     assert exl3.exl3_mx4_linear_workspace_size(4, 256, 64) >= need + 4 * 128 + 4 * 16
     assert exl3.exl3_mx4_linear_workspace_size(4, 256, 0) == 0
-    assert exl3.exl3_mx4_matmul_experts_workspace_size(4, 256, 64, 1025) == 0
+    assert exl3.exl3_mx4_matmul_experts_workspace_size(4, 256, 64, 513) == 0
 
 
 @pytest.mark.parametrize("bad", SIZES + [dict(x=None), dict(x=MIS), dict(signs=G + 8), dict(wc=None), dict(ws=None),
@@ -91,7 +91,7 @@ def test_linear_refusals(bad):
 
 
 @pytest.mark.parametrize("bad", SIZES[:3] + SIZES[4:] + [dict(off=None), dict(off=G + 4), dict(off=E), dict(experts=0),
-                                                         dict(experts=1025), dict(wc=None), dict(y=B)])
+                                                         dict(experts=513), dict(wc=None), dict(y=B)])
 def test_experts_refusals(bad):
     a = dict(xc=A, xs=B, off=G, wc=C, ws=D, y=E, dtype=0, m=4, k=256, n=64, experts=3, space=F, nb=BIG)
     a.update(bad)

@@ -46,9 +46,14 @@ constexpr int kMxBK = 512;                       // columns of k per unit: 16 sc
 constexpr int kMxBoxK = 256;                     // columns of a box: 128 bytes of codes, the swizzle's width
 constexpr int kMxMmaWarp = 0, kMxFeedWarp0 = 1;  // then 1 + groups of 128 tokens feeding warps, then the epilogue
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
-constexpr int kMxMaxExperts = 1024;
+constexpr int kMxMaxExperts = 512;
 constexpr size_t kMxSyncArea = 64 * 1024;
-constexpr int kMxSmemLimit = 232448 - 4 * (kMxMaxExperts + 1);  // what the tile table leaves
+// Shared memory of the experts' tables: each one's first tile and first row.
+constexpr int mx_table_bytes(int experts)
+{
+    return 8 * (experts + 1);
+}
+constexpr int kMxSmemLimit = 232448 - mx_table_bytes(kMxMaxExperts);
 
 // Sizes that follow from the token tile TN and the CTAs that share it (CG).
 template <int TN, int CG>
@@ -246,38 +251,40 @@ struct MxPlace {
     int ch;
 };
 
-// The rows of expert e, clamped into the buffer (the offsets are data).
-__device__ __forceinline__ void mx_expert_rows(const MxParams &p, int e, int64_t &lo, int64_t &hi)
+// The experts' tables in shared memory: the first tile and the first row of
+// each, both with one more entry.
+struct MxTables {
+    const uint32_t *tile, *row;
+    int experts;
+};
+
+// An offset clamped into the buffer (the offsets are data).
+__device__ __forceinline__ uint32_t mx_row(const MxParams &p, int e)
 {
-    lo = 0;
-    hi = p.rows;
-    if (p.offsets) {
-        const int64_t a = p.offsets[e], b = p.offsets[e + 1];
-        lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
-        hi = b < lo ? lo : (b > p.rows ? p.rows : b);
-    }
+    const int64_t r = p.offsets[e];
+    return (uint32_t)(r < 0 ? 0 : (r > p.rows ? p.rows : r));
 }
 
-// Tile t: its expert from the tiles' prefix sums (smem), then token tiles
-// fastest within a row of channels, so that neighbouring tiles share weights.
+// Tile t: its expert by bisection, then token tiles fastest within a row of
+// channels, so that neighbouring tiles share weights.
 template <int TN, int CG>
-__device__ __forceinline__ MxPlace mx_place(const MxParams &p, const uint32_t *first, uint32_t t)
+__device__ __forceinline__ MxPlace mx_place(const MxParams &p, const MxTables &tab, uint32_t t)
 {
-    int lo = 0, hi = p.experts;  // first[lo] <= t < first[hi]
+    int lo = 0, hi = tab.experts;  // tile[lo] <= t < tile[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first[mid] <= t)
+        if (tab.tile[mid] <= t)
             lo = mid;
         else
             hi = mid;
     }
-    MxPlace w;
-    int64_t r0;
-    mx_expert_rows(p, lo, r0, w.row_end);
-    const uint32_t local = t - first[lo];
-    const uint32_t tts = (uint32_t)((w.row_end - r0 + TN - 1) / TN);
+    const uint32_t r0 = tab.row[lo], r1 = tab.row[lo + 1];
+    const uint32_t local = t - tab.tile[lo];
+    const uint32_t tts = (r1 - r0 + TN - 1) / TN;
     const uint32_t nt = local / tts;
-    w.row = r0 + (int64_t)(local - nt * tts) * TN;
+    MxPlace w;
+    w.row = (int64_t)r0 + (int64_t)(local - nt * tts) * TN;
+    w.row_end = r1;
     w.ch = (int)nt * (kMxBM * CG);
     w.wrow = (int64_t)lo * p.n + w.ch;
     return w;
@@ -471,7 +478,7 @@ __device__ __forceinline__ void mx_epi_sync()
 // Segment `seg` of this worker.  Returns false if its accumulators never came
 // (the caller stops).
 template <typename T, int TN, int CG>
-__device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, const uint32_t *first, const MxSched &sched,
+__device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, const MxTables &tab, const MxSched &sched,
                                             uint32_t tmem, int seg, uint32_t rank)
 {
     using S = MxTile<TN, CG>;
@@ -482,7 +489,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     const int c0 = (warp - S::kEpiWarp0) / 4 * kCols;              // its columns
     const MxSeg g = mx_seg(sched, seg);
     const bool whole = g.k0 == 0 && g.k1 == (int)sched.KB;
-    const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+    const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
     const int acc = seg % S::kAcc;
     const uint32_t par = (uint32_t)(seg / S::kAcc) & 1u;
     bool ok = true;
@@ -669,7 +676,9 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     unsigned char *aring = smem + 1024;
     unsigned char *bring = aring + ST * kMxABytes;
     unsigned char *scales = bring + ST * S::kBBytes;
-    uint32_t *first = reinterpret_cast<uint32_t *>(scales + ST * S::kScaleBytes);  // [experts + 1]
+    uint32_t *first = reinterpret_cast<uint32_t *>(scales + ST * S::kScaleBytes);  // [experts + 1] tiles
+    uint32_t *frow = first + p.experts + 1;                                          // [experts + 1] rows
+    const MxTables tab{first, frow, p.experts};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
@@ -697,6 +706,8 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         if (early) {
             first[0] = 0;
             first[1] = nts * tts;
+            frow[0] = 0;
+            frow[1] = (uint32_t)p.rows;
         }
         fence_mbar_init();
     }
@@ -709,27 +720,36 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         grid_dep_wait();
         grid_dep_launch();
         if (warp == kMxMmaWarp && !early) {
-            // prefix sums of the experts' tiles
-            uint32_t run = 0;
-            for (int e0 = 0; e0 < p.experts; e0 += 32) {
-                uint32_t v = 0;
-                if (e0 + lane < p.experts) {
-                    int64_t lo, hi;
-                    mx_expert_rows(p, e0 + lane, lo, hi);
-                    v = (uint32_t)((hi - lo + TN - 1) / TN) * nts;
+            // prefix sums of the experts' tiles; rows that do not decrease
+            uint32_t run = 0, high = 0;
+            for (int e0 = 0; e0 <= p.experts; e0 += 32) {
+                const int e = e0 + lane;
+                uint32_t r = 0;
+                if (e <= p.experts)
+                    r = p.offsets ? mx_row(p, e) : (e ? (uint32_t)p.rows : 0u);
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t o = __shfl_up_sync(0xffffffffu, r, d);
+                    r = lane >= d && o > r ? o : r;
                 }
+                r = r > high ? r : high;
+                uint32_t before = __shfl_up_sync(0xffffffffu, r, 1);
+                before = lane ? before : high;
+                // tiles of expert e - 1, whose rows end at r
+                const uint32_t v = e >= 1 && e <= p.experts ? (r - before + TN - 1) / TN * nts : 0;
                 uint32_t incl = v;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
                     incl += lane >= d ? o : 0;
                 }
-                if (e0 + lane < p.experts)
-                    first[e0 + lane] = run + incl - v;
+                if (e <= p.experts) {
+                    first[e] = run + incl;
+                    frow[e] = r;
+                }
                 run += __shfl_sync(0xffffffffu, incl, 31);
+                high = __shfl_sync(0xffffffffu, r, 31);
             }
-            if (lane == 0)
-                first[p.experts] = run;
         }
         tc_fence_before();
         asm volatile("barrier.cta.sync 2, %0;\n" ::"n"(S::kThreads) : "memory");
@@ -838,7 +858,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         auto enter = [&]() {
             if (fseg < sched.segs) {
                 const MxSeg g = mx_seg(sched, fseg);
-                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                 fkb = g.k0;
                 fend = g.k1;
                 const int ch = (int)rank * kMxBM + lane;
@@ -873,7 +893,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                 kb = g.k0;
                 end = g.k1;
                 if (group < 0) {
-                    const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                    const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                     wrow = (int)w.wrow + (int)rank * kMxBM;
                     xrow = (int)w.row + (int)rank * S::kBRows;
                 }
@@ -895,7 +915,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             int col = 0, row = 0;
             if (mine) {
                 const MxSeg g = mx_seg(sched, seg0);
-                const MxPlace w = mx_place<TN, CG>(p, first, g.t);
+                const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                 col = (g.k0 + unit) * (kMxBK / 2);
                 row = (int)w.row;
                 mbar_arrive_expect_tx(&bars.full[lane], kMxABytes + S::kBBytes);
@@ -995,7 +1015,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     } else {
         // ---------------------------------------------------- epilogue ---
         for (int seg = 0; seg < sched.segs; ++seg)
-            if (!mx_epilogue<T, TN, CG>(p, bars, first, sched, bars.tmem_slot, seg, rank))
+            if (!mx_epilogue<T, TN, CG>(p, bars, tab, sched, bars.tmem_slot, seg, rank))
                 break;
     }
 
@@ -1079,13 +1099,13 @@ static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const C
 {
     using S = MxTile<TN, CG>;
     auto kern = mx4_gemm_kernel<T, TN, CG>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + 4 * (kMxMaxExperts + 1)) !=
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + mx_table_bytes(kMxMaxExperts)) !=
         cudaSuccess)
         return EXL3_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(workers * CG));
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = (size_t)(S::kSmem + 4 * (p.experts + 1));
+    cfg.dynamicSmemBytes = (size_t)(S::kSmem + mx_table_bytes(p.experts));
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
