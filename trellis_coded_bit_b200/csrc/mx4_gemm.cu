@@ -32,6 +32,7 @@
 // All waits are bounded; a timeout is recorded in the workspace status word,
 // and copies and MMAs in flight are drained before the CTA exits.
 #include <cuda.h>
+#include <math.h>
 
 #include "dtypes.cuh"
 #include "exl3_device.cuh"
@@ -65,7 +66,7 @@ struct MxTile {
     static constexpr int kStageBytes = kMxABytes + kBBytes + kScaleBytes;
     static constexpr int kFeedWarps = 1 + kBGroups;             // one per 128 rows of scales
     static constexpr int kEpiWarp0 = kMxFeedWarp0 + kFeedWarps;
-    static constexpr int kDepth = 3;                            // units whose scales are loaded ahead
+    static constexpr int kDepth = 2;                            // units whose scales are loaded ahead
     static constexpr int kFit = (kMxSmemLimit - 2048) / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kAcc = TN > 128 ? 1 : 2;               // accumulators in TMEM
@@ -87,6 +88,7 @@ struct MxParams {
     uint32_t *status;
     int64_t rows;               // token rows
     int n, k, kb_count, experts, stride;
+    uint32_t most;              // workers that share a split tile, at most
     uint64_t wait_ns;
 };
 
@@ -300,6 +302,9 @@ __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const MxTables &t
 // tiles instead, 74 pairs held 74 different rows of weights: 2048 x 8192 x 18944
 // took 241 us, waiting 3.4 us for each copy.)
 //
+// A split tile has at most `most` workers: its last one reads a partial sum from
+// each (mx_most_workers, on the host).
+//
 // Split tiles: `even` gives each tile floor or ceil(W / tiles) workers of its
 // own, so a worker has one segment and waits for one sum; otherwise the units
 // (tile, 256 columns) in order are cut into equal shares, and a worker may end
@@ -355,7 +360,7 @@ __device__ __forceinline__ uint32_t mx_slot(const MxSched &m, uint32_t c, uint32
     return m.even || mx_begin(m, c) >= i * m.KB ? 2 * c : 2 * c + 1;
 }
 
-__device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint32_t workers, uint32_t worker)
+__device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint32_t workers, uint32_t worker, uint32_t most)
 {
     MxSched m;
     m.worker = worker;
@@ -365,9 +370,10 @@ __device__ __forceinline__ MxSched mx_schedule(uint32_t tiles, uint32_t KB, uint
     m.split0 = m.whole * workers;
     m.splits = tiles - m.split0;
     m.U = m.splits * KB;
-    // no more workers than units: with an empty share between two others a
-    // tile's segments would be miscounted
+    // no more workers than units (with an empty share between two others a
+    // tile's segments would be miscounted), and `most` for a tile
     m.W = m.U < workers ? m.U : workers;
+    m.W = m.W < m.splits * most ? m.W : m.splits * most;
     m.u0 = m.u1 = 0;
     m.split_segs = 0;
     m.even = false;
@@ -602,7 +608,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     if (bars.ticket) {
         // sums in segment order, this CTA's own from TMEM; kAhead segments'
         // loads of 16 columns in flight
-        constexpr int kAhead = TN >= 128 ? 2 : 4;
+        constexpr int kAhead = TN > 128 ? 2 : 4;  // (4 spilled the registers of whole tiles)
         const int own = (int)(sched.worker - c_lo);
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16) {
@@ -758,7 +764,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         tc_fence_after();
     }
     const int KB = p.kb_count;
-    const MxSched sched = mx_schedule(early ? nts * tts : first[p.experts], (uint32_t)KB, gridDim.x / CG, worker);
+    const MxSched sched = mx_schedule(early ? nts * tts : first[p.experts], (uint32_t)KB, gridDim.x / CG, worker, p.most);
 
     if (warp == kMxMmaWarp) {
         if (rank == 0 && sched.segs > 0) {
@@ -847,8 +853,8 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         // the 128 weight rows, the others those of 128 token rows each.  Lane
         // l owns rows l, l + 32, l + 64, l + 96, whose scales of 128 columns
         // are the 16 bytes at 16 l of the layout that the tensor core wants:
-        // one conflict-free store.  It loads a unit's 16 scales of each row
-        // kDepth units ahead into registers.
+        // one conflict-free store.  It loads a unit's 16 scales of each row up
+        // to kDepth units ahead into registers.
         const int group = warp - kMxFeedWarp0 - 1;  // -1: weights
         const int kblocks = p.k / kMx4Block;
         // load side: segment, unit and rows of the next step
@@ -991,7 +997,12 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                             next();
                         }
                     }
-                    fetch(q[d]);
+                    // two units at a time: their 16 bytes of a row are one
+                    // 32-byte sector, which then crosses from L2 once
+                    if (d & 1) {
+                        fetch(q[d - 1]);
+                        fetch(q[d]);
+                    }
                 }
             }
         }
@@ -1068,23 +1079,37 @@ static bool code_map(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Token tile for `rows` tokens per expert: the narrowest that takes them in
-// one tile, up to the widest.
-static int mx_token_tile(int64_t rows)
+// Token tile for `rows` rows over `experts` experts: the narrowest of 16 .. 128
+// that takes an average expert's in one tile.  Above that, 256 tokens x 256
+// channels on a pair of CTAs move the fewest bytes per product (1.8 against 1.5
+// 128 x 128 x 512 products per SM and us), but leave pairs idle or split where
+// tiles are few; from two tiles a pair on they win (us, 128 wide / 256 wide):
+// 2048 x 8192 x 8192 (3.5 tiles a pair) 81 / 72, 2048 x 8192 x 28672 262 / 219;
+// 2048 x 2048 x 8192 (0.9) 34 / 42, 333 x 4000 x 10001 (1.1) 25 / 34.
+static int mx_token_tile(int64_t rows, int64_t n, int64_t experts)
 {
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int64_t each = (rows + experts - 1) / experts;
+    if (each <= 128)
+        return each <= 16 ? 16 : each <= 32 ? 32 : each <= 64 ? 64 : 128;
+    const int64_t tiles = (rows + 255) / 256 * ((n + 255) / 256);
+    return tiles >= num_sms() ? 256 : 128;
 }
 
-// Rows of an average expert, rounded up.
-static int64_t mx_rows_each(int64_t rows, int64_t experts)
+// Workers that may share a tile of kb units: w of them take kb/w units each and
+// then w partial sums of TN x 128 per CTA to add, so w = sqrt(kb unit/partial).
+// A unit takes 1.1 us (256 tokens), 0.7 us (fewer), a partial written and read
+// 0.35 us and 0.012 us a token: 333 x 4000 x 10001 with 8 workers on each of 6
+// left-over tiles took 44 us, with 2 a half.
+static uint32_t mx_most_workers(int tn, int kb)
 {
-    return (rows + experts - 1) / experts;
+    const double unit = tn > 128 ? 1.1 : 0.7, partial = 0.35 + 0.012 * tn;
+    const double w = sqrt(kb * unit / partial);
+    return w < 1.0 ? 1u : (uint32_t)w;
 }
 
-static size_t mx_workspace(int64_t rows, int64_t experts)
+static size_t mx_workspace(int64_t rows, int64_t n, int64_t experts)
 {
-    const int tn = mx_token_tile(mx_rows_each(rows, experts));
-    return kMxSyncArea + (size_t)2 * num_sms() * tn * kMxBM * 4;
+    return kMxSyncArea + (size_t)2 * num_sms() * mx_token_tile(rows, n, experts) * kMxBM * 4;
 }
 
 static bool valid_mx_sizes(int64_t m, int64_t k, int64_t n, int64_t experts)
@@ -1163,7 +1188,7 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
                           const uint8_t *ws, void *y, int dtype, int64_t m, int64_t k, int64_t n, int64_t experts,
                           void *workspace, bool pdl, cudaStream_t s)
 {
-    const int tn = mx_token_tile(mx_rows_each(m, experts));
+    const int tn = mx_token_tile(m, n, experts);
     const int cg = tn > 128 ? 2 : 1;  // CTAs that share a tile
     CUtensorMap wmap, xmap;
     if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, xc, m, k / 2, tn / cg))
@@ -1182,6 +1207,7 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     p.kb_count = (int)((k + kMxBK - 1) / kMxBK);
     p.experts = (int)experts;
     p.stride = (int)mx4_scale_stride(k);
+    p.most = mx_most_workers(tn, p.kb_count);
     p.wait_ns = wait_limit_ns();
     // units fit 32 bits: at most (rows/TN + experts) tiles of each channel row
     const int64_t tiles =
@@ -1200,10 +1226,10 @@ struct MxLinearPlan {
     size_t codes, scales, total;
 };
 
-static MxLinearPlan mx_linear_plan(int64_t m, int64_t k)
+static MxLinearPlan mx_linear_plan(int64_t m, int64_t k, int64_t n)
 {
     MxLinearPlan pl;
-    pl.codes = (mx_workspace(m, 1) + 255) / 256 * 256;
+    pl.codes = (mx_workspace(m, n, 1) + 255) / 256 * 256;
     pl.scales = pl.codes + ((size_t)m * (size_t)(k / 2) + 255) / 256 * 256;
     pl.total = pl.scales + (size_t)m * (size_t)mx4_scale_stride(k);
     return pl;
@@ -1213,7 +1239,7 @@ static MxLinearPlan mx_linear_plan(int64_t m, int64_t k)
 
 extern "C" size_t exl3_mx4_matmul_workspace_size(int64_t m, int64_t k, int64_t n)
 {
-    return exl3::valid_mx_sizes(m, k, n, 1) ? exl3::mx_workspace(m, 1) : 0;
+    return exl3::valid_mx_sizes(m, k, n, 1) ? exl3::mx_workspace(m, n, 1) : 0;
 }
 
 extern "C" exl3_status exl3_mx4_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws,
@@ -1224,14 +1250,14 @@ extern "C" exl3_status exl3_mx4_matmul(const uint8_t *xc, const uint8_t *xs, con
     const exl3_status st = check_mx(xc, xs, wc, ws, y, dtype, m, k, n, 1);
     if (st != EXL3_OK || m == 0)
         return st;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(m, 1))
+    if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(m, n, 1))
         return EXL3_ERR_WORKSPACE;
     return run_mx(xc, xs, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t exl3_mx4_matmul_experts_workspace_size(int64_t rows, int64_t k, int64_t n, int64_t experts)
 {
-    return exl3::valid_mx_sizes(rows, k, n, experts) ? exl3::mx_workspace(rows, experts) : 0;
+    return exl3::valid_mx_sizes(rows, k, n, experts) ? exl3::mx_workspace(rows, n, experts) : 0;
 }
 
 extern "C" exl3_status exl3_mx4_matmul_experts(const uint8_t *xc, const uint8_t *xs, const int32_t *offsets,
@@ -1246,14 +1272,14 @@ extern "C" exl3_status exl3_mx4_matmul_experts(const uint8_t *xc, const uint8_t 
     if (!offsets || !aligned16(offsets) ||
         ranges_overlap(offsets, (size_t)(experts + 1) * 4, y, (size_t)rows * (size_t)n * 2))
         return EXL3_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(rows, experts))
+    if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(rows, n, experts))
         return EXL3_ERR_WORKSPACE;
     return run_mx(xc, xs, offsets, wc, ws, y, dtype, rows, k, n, experts, workspace, false, (cudaStream_t)stream);
 }
 
 extern "C" size_t exl3_mx4_linear_workspace_size(int64_t m, int64_t k, int64_t n)
 {
-    return exl3::valid_mx_sizes(m, k, n, 1) ? exl3::mx_linear_plan(m, k).total : 0;
+    return exl3::valid_mx_sizes(m, k, n, 1) ? exl3::mx_linear_plan(m, k, n).total : 0;
 }
 
 extern "C" exl3_status exl3_mx4_linear(const void *x, int dtype, const void *signs, int rotate, const uint8_t *wc,
@@ -1269,7 +1295,7 @@ extern "C" exl3_status exl3_mx4_linear(const void *x, int dtype, const void *sig
         ranges_overlap(x, (size_t)m * (size_t)k * 2, y, (size_t)m * (size_t)n * 2) ||
         (signs && ranges_overlap(signs, (size_t)k * 2, y, (size_t)m * (size_t)n * 2)))
         return EXL3_ERR_INVALID_ARG;
-    const MxLinearPlan pl = mx_linear_plan(m, k);
+    const MxLinearPlan pl = mx_linear_plan(m, k, n);
     if (!workspace || !aligned16(workspace) || workspace_bytes < pl.total)
         return EXL3_ERR_WORKSPACE;
     uint8_t *base = (uint8_t *)workspace;
