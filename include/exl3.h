@@ -42,7 +42,8 @@
  *     aligned; the library never allocates, frees or synchronises inside these
  *     calls.  Work is enqueued asynchronously on `stream` (a cudaStream_t;
  *     NULL = the legacy default stream).
- *   - k and n must be multiples of 128; 1 <= K <= 8; y must not overlap x.
+ *   - Layers of trellis weights have k and n multiples of 128 and 1 <= K <= 8.
+ *     Outputs must not overlap inputs unless a call says so.
  *   - Argument errors return EXL3_ERR_INVALID_ARG / EXL3_ERR_UNSUPPORTED /
  *     EXL3_ERR_WORKSPACE before anything is launched.  A failed launch returns
  *     EXL3_ERR_CUDA (the CUDA error is left for cudaGetLastError to report).
@@ -482,7 +483,8 @@ exl3_status exl3_moe_combine_grad(const void *dy, const void *ys, int dtype, con
  * EXL3_LAUNCH_PDL -- launch exl3_gemv / exl3_gemm kernels with programmatic
  *   dependent launch (CUDA programmatic stream serialization): a kernel may
  *   start while the preceding kernel in the stream is still finishing, and
- *   it begins streaming its WEIGHT operands (trellis, suh, svh) at once; all
+ *   it begins streaming its WEIGHT operands (trellis, suh, svh; 4-bit w codes
+ *   and scales) at once; all
  *   other reads (x, the workspace) and every write wait until the preceding
  *   kernel has completed and its writes are visible.  Enable it only when the
  *   weights are not written by the kernel launched immediately before on the

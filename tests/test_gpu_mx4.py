@@ -204,7 +204,9 @@ def product(x, w, dtype, ws=None, **kw):
 SHAPES = [(1, 32, 1), (1, 256, 128), (1, 64, 5), (2, 96, 129), (16, 128, 128), (17, 288, 130), (15, 512, 64),
           (32, 1024, 200), (33, 256, 384), (64, 544, 257), (65, 2048, 100), (128, 320, 256), (129, 768, 300),
           (200, 4096, 128), (256, 256, 256), (257, 160, 131), (300, 4000, 1000), (1, 4096, 4096), (8, 14336, 512),
-          (513, 512, 640), (40, 8192, 77)]
+          (513, 512, 640), (40, 8192, 77),
+          # pairs of CTAs: whole tiles, split tiles, odd rows and channels
+          (520, 1536, 13001), (1100, 544, 9100), (2100, 96, 4360)]
 
 
 @pytest.mark.parametrize("m,k,n", SHAPES)
@@ -217,6 +219,8 @@ def test_product_exact_with_equal_scales(m, k, n):
     assert np.abs(ref).max() < 60000
     for dtype in (torch.float16, torch.bfloat16):
         assert torch.equal(product(x, w, dtype).cpu(), torch.from_numpy(ref).to(dtype))
+    if m * n > 1 << 20:  # the same on pairs of CTAs or not: bit for bit on every call
+        assert torch.equal(product(x, w, torch.float16), product(x, w, torch.float16))
 
 
 @pytest.mark.parametrize("m,k,n", SHAPES)
@@ -324,7 +328,8 @@ def experts_case(rng, counts, k, n, spare=0, low=120, high=127):
 
 @pytest.mark.parametrize("counts,k,n,spare", [([1], 64, 20, 0), ([0, 3, 0, 0, 1], 256, 130, 2), ([5, 0, 17, 2], 544, 100, 1),
                                               ([40, 1, 0, 90, 16], 512, 256, 0), ([300, 2, 130], 1024, 128, 7),
-                                              ([0, 0], 128, 64, 4), ([1] * 40, 256, 48, 0), ([700, 1, 300], 256, 200, 0)])
+                                              ([0, 0], 128, 64, 4), ([1] * 40, 256, 48, 0), ([700, 1, 300], 256, 200, 0),
+                                              ([900, 0, 257, 1500, 3, 640], 512, 3000, 5), ([200] * 16, 288, 2600, 0)])
 def test_experts(counts, k, n, spare):
     rng = np.random.default_rng(sum(counts) + k)
     offsets, x, w = experts_case(rng, counts, k, n, spare)
@@ -393,10 +398,11 @@ def test_expert_layer():
 
 # ------------------------------------------------------------ how it is called ---
 
-def test_timeout_is_reported_and_cleared():
+@pytest.mark.parametrize("m,k,n", [(20, 2048, 2000), (600, 2048, 14000)])  # single CTAs, and pairs
+def test_timeout_is_reported_and_cleared(m, k, n):
     rng = np.random.default_rng(30)
-    x, w = operand(rng, 20, 2048), operand(rng, 2000, 2048)
-    ws = exl3.new_workspace(exl3.exl3_mx4_matmul_workspace_size(20, 2048, 2000))
+    x, w = operand(rng, m, k), operand(rng, n, k)
+    ws = exl3.new_workspace(exl3.exl3_mx4_matmul_workspace_size(m, k, n))
     xc, xs = (dev(a) for a in mx4.pack(*x))
     wc, wsc = (dev(a) for a in mx4.pack(*w))
     exl3.exl3_debug_set_wait_limit_ns(1)
@@ -407,7 +413,8 @@ def test_timeout_is_reported_and_cleared():
         exl3.exl3_debug_set_wait_limit_ns(0)
     y = exl3.exl3_mx4_matmul(xc, xs, wc, wsc, workspace=ws)
     assert exl3.exl3_workspace_status(ws) == exl3.EXL3_OK
-    assert torch.equal(y.cpu(), torch.from_numpy(mx4.values(*x) @ mx4.values(*w).T).half())
+    cols = rng.integers(0, n, 500)
+    assert torch.equal(y[:, dev(cols)].cpu(), torch.from_numpy(mx4.values(*x) @ mx4.values(*w)[cols].T).half())
 
 
 @pytest.mark.parametrize("flags", [0, exl3.EXL3_LAUNCH_PDL])
