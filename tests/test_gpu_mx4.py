@@ -298,23 +298,49 @@ def test_product_large_and_repeatable():
                        torch.from_numpy(mx4.values(*x2) @ mx4.values(*w2).T).half())
 
 
+@pytest.mark.parametrize("dtype", TYPES[:2])
 @pytest.mark.parametrize("m,k,n,rotate", [(1, 4096, 512, True), (5, 256, 130, True), (70, 1024, 200, False),
-                                          (1, 96, 33, False), (300, 512, 256, True)])
-def test_linear_is_quantize_then_product(m, k, n, rotate):
+                                          (1, 96, 33, False), (300, 512, 256, True), (2, 128, 40, True), (2, 1152, 4200, True),
+                                          (2, 32, 300, False), (1, 1056, 129, False), (1, 14336, 640, True), (3, 640, 128, True)])
+def test_linear_is_quantize_then_product(dtype, m, k, n, rotate):
     rng = np.random.default_rng(m + n)
-    x = torch.from_numpy(rng.standard_normal((m, k))).half().cuda()
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(dtype).cuda()
+    x[0, 7] = 0.0
     signs = torch.from_numpy(rng.choice([-1.0, 1.0], k)).half().cuda() if rotate else None
     wm = rng.standard_normal((n, k)) * 0.02
     wc, wsc = exl3.exl3_mx4_quantize(torch.from_numpy(wm).float().cuda(), signs=signs, rotate=rotate)
     ws = exl3.new_workspace(exl3.exl3_mx4_linear_workspace_size(m, k, n))
     y = exl3.exl3_mx4_linear(x, wc, wsc, signs=signs, rotate=rotate, workspace=ws)
     xc, xs = exl3.exl3_mx4_quantize(x, signs=signs, rotate=rotate)
-    assert torch.equal(y, exl3.exl3_mx4_matmul(xc, xs, wc, wsc, workspace=ws))
+    assert torch.equal(y, exl3.exl3_mx4_matmul(xc, xs, wc, wsc, dtype=dtype, workspace=ws))
     # and it is the layer: the rotation cancels, what is left is the rounding
     # of both operands (relative 4-bit errors near 0.1 each, independent)
     if m * n > 500 and rotate:
         ref = host(x) @ wm.T
         assert np.linalg.norm(host(y) - ref) <= 0.25 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("m", [1, 2, 9])
+def test_linear_of_infinities_and_values_beside_borders(m):
+    """A row with an infinity becomes NaN and leaves the others alone; a row
+    whose rotated values lie on rounding borders takes the exact path."""
+    rng = np.random.default_rng(50 + m)
+    k, n = 512, 300
+    x = np.zeros((m, k), dtype=np.float16)
+    x[0, 0::128] = 1.0     # every rotated value 1/sqrt(128): the scale's border
+    x[0, 130] = 2.0
+    if m > 1:
+        x[1, 5] = np.inf
+    wc, wsc = exl3.exl3_mx4_quantize(torch.from_numpy(rng.standard_normal((n, k))).float().cuda())
+    ws = exl3.new_workspace(exl3.exl3_mx4_linear_workspace_size(m, k, n))
+    y = exl3.exl3_mx4_linear(dev(x), wc, wsc, rotate=True, workspace=ws)
+    xc, xs = exl3.exl3_mx4_quantize(dev(x), rotate=True)
+    assert torch.equal(y[0], exl3.exl3_mx4_matmul(xc, xs, wc, wsc, workspace=ws)[0])
+    assert torch.isfinite(y[0]).all() and (m == 1 or torch.isnan(y[1]).all()) and torch.isfinite(y[2:]).all()
+    xq = mx4.values(*mx4.quantize(mx4.rotate(x[:1])))
+    ref = xq @ mx4.values(*unpacked(wc, wsc)).T
+    mag = np.abs(xq) @ np.abs(mx4.values(*unpacked(wc, wsc))).T
+    assert np.all(np.abs(host(y[:1]) - ref) <= 2.0 ** -11 * np.abs(ref) + k * 2.0 ** -23 * mag + 2.0 ** -25)
 
 
 # ----------------------------------------------------------------- experts ---

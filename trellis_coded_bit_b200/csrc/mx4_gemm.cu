@@ -38,6 +38,7 @@
 #include "exl3_device.cuh"
 #include "exl3_host.h"
 #include "mx4.cuh"
+#include "mx4_quantize.cuh"
 #include "tcgen05.cuh"
 
 namespace exl3 {
@@ -48,6 +49,7 @@ constexpr int kMxBoxK = 256;                     // columns of a box: 128 bytes 
 constexpr int kMxMmaWarp = 0, kMxFeedWarp0 = 1;  // then 1 + groups of 128 tokens feeding warps, then the epilogue
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
 constexpr int kMxMaxExperts = 512;
+constexpr int kMxFuseRows = 2;                   // tokens that the product of a layer quantises itself
 constexpr size_t kMxSyncArea = 64 * 1024;
 // Shared memory of the experts' tables: each one's first tile and first row.
 constexpr int mx_table_bytes(int experts)
@@ -90,6 +92,10 @@ struct MxParams {
     int n, k, kb_count, experts, stride;
     uint32_t most;              // workers that share a split tile, at most
     uint64_t wait_ns;
+    // FUSE: the activations themselves
+    const void *x;
+    const __half *signs;
+    int rotate;
 };
 
 struct MxBars {
@@ -670,7 +676,12 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
 
 // --------------------------------------------------------- main kernel ---
 
-template <typename T, int TN, int CG>
+// FUSE: the tokens (kMxFuseRows at most) come as rows of T, and the warp that
+// would deal out their scales quantises them, codes and scales, straight into
+// the stage: 4 lanes a rotation, 16 a token and unit, so one pass of the warp a
+// unit.  Every CTA repeats it for its units; the weights' bytes still bound the
+// unit, and a launch and its 3 us are gone.
+template <typename T, int TN, int CG, bool FUSE>
 __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     mx4_gemm_kernel(const MxParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
@@ -846,6 +857,55 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             if (!ok && lane == 0)
                 record_timeout(p.status);
         }
+    } else if (FUSE && warp == kMxFeedWarp0 + 1) {
+        // ----------------------------------- quantising a token or two ---
+        // Lane: block `lane & 3` of 32 columns of the unit's 128-column group
+        // (lane >> 2) & 3 of token lane >> 4.
+        const int l = lane & 3, grp = (lane >> 2) & 3, row = lane >> 4;
+        const bool mine = row < (int)p.rows;
+        const T *const xr = (const T *)p.x + (int64_t)(mine ? row : 0) * p.k;
+        int s = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (int seg = 0; seg < sched.segs && ok; ++seg) {
+            const MxSeg g = mx_seg(sched, seg);
+            for (int kb = g.k0; kb < g.k1 && ok; ++kb) {
+                const int col = kb * kMxBK + 128 * grp + 32 * l;
+                const bool there = col < p.k;  // with the rotation k ends with a group of 128
+                const int at = there ? col : 32 * l < p.k ? 32 * l : 0;
+                int byte = 0;
+                uint4 code;
+                if (p.rotate)
+                    code = quantize_block_rotated<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
+                else
+                    code = quantize_block<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
+                if (!there) {
+                    code = make_uint4(0u, 0u, 0u, 0u);
+                    byte = 0;
+                }
+                ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
+                if (!ok)
+                    break;
+                if (mine) {
+                    // row `row` of the box of columns 256 (grp / 2) on, 16-byte
+                    // chunk 4 (grp % 2) + l, at the place the swizzle gives it
+                    const int chunk = 4 * (grp & 1) + l;
+                    *reinterpret_cast<uint4 *>(bring + s * S::kBBytes + (grp >> 1) * (S::kBBytes / 2) + row * 128 +
+                                               ((chunk ^ (row & 7)) << 4)) = code;
+                    scales[s * S::kScaleBytes + 2048 + 512 * grp + row * 16 + l] = (unsigned char)byte;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.full[s]);
+                if (++s == ST) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok && lane == 0)
+            record_timeout(p.status);
     } else if (warp < S::kEpiWarp0) {
         // ----------------------------------------------------- feeding ---
         // Warp 0 of these issues the copies of the codes (both CTAs' bytes of
@@ -924,7 +984,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                 const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                 col = (g.k0 + unit) * (kMxBK / 2);
                 row = (int)w.row;
-                mbar_arrive_expect_tx(&bars.full[lane], kMxABytes + S::kBBytes);
+                mbar_arrive_expect_tx(&bars.full[lane], kMxABytes + (FUSE ? 0 : S::kBBytes));
                 for (int h = 0; h < 2; ++h)
                     tma_load_2d<CG>(aring + lane * kMxABytes + h * (kMxABytes / 2), &wmap, col + h * (kMxBoxK / 2),
                                     (int)w.wrow, smem_addr(&bars.full[lane]));
@@ -932,7 +992,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             pre = __popc(__ballot_sync(0xffffffffu, mine));
             grid_dep_wait();
             grid_dep_launch();
-            if (mine)
+            if (mine && !FUSE)
                 for (int h = 0; h < 2; ++h)
                     tma_load_2d<CG>(bring + lane * S::kBBytes + h * (S::kBBytes / 2), &xmap, col + h * (kMxBoxK / 2), row,
                                     smem_addr(&bars.full[lane]));
@@ -952,12 +1012,13 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                             const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
                             if (elect_one()) {
                                 if (rank == 0)
-                                    mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + S::kBBytes));
+                                    mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + (FUSE ? 0 : S::kBBytes)));
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
                                     tma_load_2d<CG>(aring + s * kMxABytes + h * (kMxABytes / 2), &wmap, col, wrow, bar);
-                                    tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
+                                    if constexpr (!FUSE)
+                                        tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
                                 }
                             }
                             __syncwarp();
@@ -1118,12 +1179,12 @@ static bool valid_mx_sizes(int64_t m, int64_t k, int64_t n, int64_t experts)
            experts <= kMxMaxExperts && experts * n <= (int64_t)1 << 30;
 }
 
-template <typename T, int TN, int CG>
+template <typename T, int TN, int CG, bool FUSE = false>
 static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap, int workers, bool pdl,
                              cudaStream_t s)
 {
     using S = MxTile<TN, CG>;
-    auto kern = mx4_gemm_kernel<T, TN, CG>;
+    auto kern = mx4_gemm_kernel<T, TN, CG, FUSE>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + mx_table_bytes(kMxMaxExperts)) !=
         cudaSuccess)
         return EXL3_ERR_CUDA;
@@ -1155,6 +1216,8 @@ template <typename T>
 static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap,
                                   int workers, bool pdl, cudaStream_t s)
 {
+    if (p.x)
+        return launch_mx<T, 16, 1, true>(p, wmap, xmap, workers, pdl, s);
     switch (tn) {
     case 16: return launch_mx<T, 16, 1>(p, wmap, xmap, workers, pdl, s);
     case 32: return launch_mx<T, 32, 1>(p, wmap, xmap, workers, pdl, s);
@@ -1186,14 +1249,19 @@ static exl3_status check_mx(const uint8_t *xc, const uint8_t *xs, const uint8_t 
 
 static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *offsets, const uint8_t *wc,
                           const uint8_t *ws, void *y, int dtype, int64_t m, int64_t k, int64_t n, int64_t experts,
-                          void *workspace, bool pdl, cudaStream_t s)
+                          void *workspace, bool pdl, cudaStream_t s, const void *x = nullptr,
+                          const void *signs = nullptr, int rotate = 0)
 {
     const int tn = mx_token_tile(m, n, experts);
     const int cg = tn > 128 ? 2 : 1;  // CTAs that share a tile
     CUtensorMap wmap, xmap;
-    if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, xc, m, k / 2, tn / cg))
+    // (with x the tokens' map is not used)
+    if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, x ? wc : xc, x ? n : m, k / 2, tn / cg))
         return EXL3_ERR_CUDA;
     MxParams p;
+    p.x = x;
+    p.signs = (const __half *)signs;
+    p.rotate = rotate;
     p.xs = xs;
     p.ws = ws;
     p.offsets = offsets;
@@ -1296,6 +1364,7 @@ extern "C" exl3_status exl3_mx4_linear(const void *x, int dtype, const void *sig
         (signs && ranges_overlap(signs, (size_t)k * 2, y, (size_t)m * (size_t)n * 2)))
         return EXL3_ERR_INVALID_ARG;
     const MxLinearPlan pl = mx_linear_plan(m, k, n);
+    const bool fuse = m <= kMxFuseRows;
     if (!workspace || !aligned16(workspace) || workspace_bytes < pl.total)
         return EXL3_ERR_WORKSPACE;
     uint8_t *base = (uint8_t *)workspace;
@@ -1303,6 +1372,9 @@ extern "C" exl3_status exl3_mx4_linear(const void *x, int dtype, const void *sig
     const exl3_status st = check_mx(xc, xs, wc, ws, y, dtype, m, k, n, 1);
     if (st != EXL3_OK)
         return st;
+    if (fuse)
+        return run_mx(nullptr, nullptr, nullptr, wc, ws, y, dtype, m, k, n, 1, workspace, false, (cudaStream_t)stream, x,
+                      signs, rotate);
     const exl3_status q = exl3_mx4_quantize(x, dtype, signs, rotate, nullptr, 1, m, xc, xs, m, k, stream);
     if (q != EXL3_OK)
         return q;
