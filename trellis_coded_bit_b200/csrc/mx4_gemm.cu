@@ -12,22 +12,27 @@
 // both the decode (bound by the weights' bytes) and the prompt (bound by the
 // tensor cores).
 //
-// Persistent and stream-K balanced: the work units are (128 channels x TN
-// tokens, 256 columns of k) in tile order and CTA c of G owns units
-// [cU/G, (c+1)U/G).  A tile whose units fall to several CTAs meets in the
-// workspace: each segment writes its fp32 partial sums, the last to arrive
-// (atomic ticket, no spinning) adds them in segment order and writes y, so
-// results are deterministic.  A tile that is split is the last of exactly one
-// CTA's range that begins it, so that CTA's number indexes its ticket.
+// Persistent, one CTA per SM.  The work units are (128 channels x TN tokens, 512
+// columns of k); above 128 tokens a tile is 256 channels x 256 tokens on a pair of
+// CTAs (tcgen05 cta_group::2: each holds its 128 channels and half the tokens'
+// codes, and the pair's MMAs read both), which moves a third fewer bytes per
+// product.  mx_schedule says how tiles are shared out; where several workers share
+// one, each writes its fp32 partial sums and the last to arrive (atomic ticket, no
+// spinning) adds them in a fixed order, so results are deterministic.
 //
-// Warps: 0 TMA producer (weight and token codes, 128-byte swizzled boxes of
-// 256 columns), 1 MMA issuer, 2..5 scales, 6..9 epilogue.  Scales are row-major
-// in memory; the tensor core wants, per 128 columns and 128 rows, 512 bytes
-// with row r's 4 scales at 16 (r % 32) + 4 (r / 32).  A scale thread owns a
-// row: it copies 16 scales (512 columns) at a time into a private ring
-// (cp.async, several steps ahead) and deals them out to the stages;
-// tcgen05.cp then broadcasts a stage's scales to the TMEM columns that belong
-// to the stage.
+// Warps: 0 MMA issuer, 1 copies (TMA, 128-byte swizzled boxes of 256 columns), 2
+// and 3 scales, 4 .. epilogue.  Scales are row-major in memory; the tensor core
+// wants, per 128 columns and 128 rows, 512 bytes with row r's 4 scales at
+// 16 (r % 32) + 4 (r / 32).  The scale warps load them a few units ahead, deal
+// them out to the stages in that order, and tcgen05.cp broadcasts a stage's to the
+// TMEM columns that belong to the stage.
+//
+// What bounds it: few tokens, the weights' bytes (32 x 8192 x 28672: 28 us, 4.5
+// TB/s, of which 19 us are the bytes and most of the rest the first copy's 2.6 us,
+// the start, and the sums of split tiles); many, the supply of the tensor cores at
+// the ends of tiles (2048 x 8192 x 28672: 201 us, 4.8 PFLOP/s; within a tile a unit
+// takes 1050 cycles, the MMAs' own time, and while the tile before is stored
+// 2000).
 //
 // All waits are bounded; a timeout is recorded in the workspace status word,
 // and copies and MMAs in flight are drained before the CTA exits.
@@ -46,7 +51,7 @@ namespace exl3 {
 constexpr int kMxBM = 128;                       // output channels per CTA's tile (TMEM lanes)
 constexpr int kMxBK = 512;                       // columns of k per unit: 16 scales of a row, two boxes of codes
 constexpr int kMxBoxK = 256;                     // columns of a box: 128 bytes of codes, the swizzle's width
-constexpr int kMxMmaWarp = 0, kMxFeedWarp0 = 1;  // then 1 + groups of 128 tokens feeding warps, then the epilogue
+constexpr int kMxMmaWarp = 0, kMxTmaWarp = 1, kMxScaleWarp0 = 2, kMxEpiWarp0 = 4;
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
 constexpr int kMxMaxExperts = 512;
 constexpr int kMxFuseRows = 2;                   // tokens that the product of a layer quantises itself
@@ -66,8 +71,7 @@ struct MxTile {
     static constexpr int kBGroups = (TN + 127) / 128;           // 128-row groups of token scales
     static constexpr int kScaleBytes = 2048 + kBGroups * 2048;  // four 128-column chunks of 512 bytes per group
     static constexpr int kStageBytes = kMxABytes + kBBytes + kScaleBytes;
-    static constexpr int kFeedWarps = 1 + kBGroups;             // one per 128 rows of scales
-    static constexpr int kEpiWarp0 = kMxFeedWarp0 + kFeedWarps;
+    static constexpr int kScaleRows = TN > 128 ? 6 : 4;         // rows of scales of a scale warp's lane
     static constexpr int kDepth = 2;                            // units whose scales are loaded ahead
     static constexpr int kFit = (kMxSmemLimit - 2048) / kStageBytes;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -76,7 +80,7 @@ struct MxTile {
     static constexpr int kAccCols = TN < 32 ? 32 : TN;
     static constexpr int kEpiWarps = TN >= 128 ? 8 : 4;         // each: 32 lanes x kEpiCols columns
     static constexpr int kEpiCols = TN / (kEpiWarps / 4);
-    static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+    static constexpr int kThreads = 32 * (kMxEpiWarp0 + kEpiWarps);
     static constexpr int kSmem = 2048 + kStages * kStageBytes;
     static_assert(kAcc * kAccCols + kStages * kScaleCols <= 512, "TMEM columns");
 };
@@ -498,7 +502,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     volatile int *epi_abort = &bars.epi_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quarter = warp & 3;                                  // TMEM lanes this warp may access
-    const int c0 = (warp - S::kEpiWarp0) / 4 * kCols;              // its columns
+    const int c0 = (warp - kMxEpiWarp0) / 4 * kCols;              // its columns
     const MxSeg g = mx_seg(sched, seg);
     const bool whole = g.k0 == 0 && g.k1 == (int)sched.KB;
     const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
@@ -568,9 +572,16 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                 mbar_arrive_leader(&bars.acc_empty[acc]);
         }
         if (wide && cols == kCols && ch_left >= 32) {
+            // Pairs: the stores are spread over about a third of the next tile's
+            // main loop; in one burst they held up its scales' loads (4096 x 4096
+            // x 14336: 117 us, without pauses 123).
+            const bool pace = CG == 2 && sched.KB >= 4 && seg + 1 < sched.segs;
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8)
+            for (int c = 0; c < kCols; c += 8) {
                 mx_store8<T, true>(y + (int64_t)c * p.n, p.n, v + c / 2, 8, 32, true);
+                if (pace)
+                    __nanosleep(sched.KB * 12);
+            }
             return true;
         }
 #pragma unroll
@@ -600,7 +611,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                                    __uint_as_float(b[4 * g + 2]), __uint_as_float(b[4 * g + 3])));
     }
     mx_epi_sync<TN, CG>();
-    if (threadIdx.x == 32 * S::kEpiWarp0) {
+    if (threadIdx.x == 32 * kMxEpiWarp0) {
         // the barrier orders the other threads' partials before this fence
         __threadfence();
         uint32_t *counter = &p.counters[split * CG + rank];
@@ -701,16 +712,16 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     const uint32_t worker = blockIdx.x / CG;
     // Without experts the tiles are known at once, and the warp that issues the
-    // copies waits for nobody: it sets up the barriers, begins the first stages
-    // and loads its first scales while the others set up.  What it reads before
-    // grid_dep_wait are weights alone.
+    // copies waits for nobody: it sets up the barriers and begins the first stages
+    // while the others set up.  What it reads before grid_dep_wait are weights
+    // alone.
     const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
     const uint32_t tts = (uint32_t)((p.rows + TN - 1) / TN);  // without experts
     const bool early = CG == 1 && !p.offsets;
-    const bool ahead = early && warp == kMxFeedWarp0;
-    if (threadIdx.x == 32 * kMxFeedWarp0) {
+    const bool ahead = early && warp == kMxTmaWarp;
+    if (threadIdx.x == 32 * kMxTmaWarp) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&bars.full[s], 1 + CG * S::kFeedWarps);  // the bytes, each CTA's scales
+            mbar_init(&bars.full[s], 1 + CG * 2);  // the bytes, each CTA's scale warps
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -857,7 +868,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             if (!ok && lane == 0)
                 record_timeout(p.status);
         }
-    } else if (FUSE && warp == kMxFeedWarp0 + 1) {
+    } else if (FUSE && warp == kMxScaleWarp0 + 1) {
         // ----------------------------------- quantising a token or two ---
         // Lane: block `lane & 3` of 32 columns of the unit's 128-column group
         // (lane >> 2) & 3 of token lane >> 4.
@@ -906,67 +917,12 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
         }
         if (!ok && lane == 0)
             record_timeout(p.status);
-    } else if (warp < S::kEpiWarp0) {
-        // ----------------------------------------------------- feeding ---
-        // Warp 0 of these issues the copies of the codes (both CTAs' bytes of
-        // a stage count on the leader's barrier) and deals out the scales of
-        // the 128 weight rows, the others those of 128 token rows each.  Lane
-        // l owns rows l, l + 32, l + 64, l + 96, whose scales of 128 columns
-        // are the 16 bytes at 16 l of the layout that the tensor core wants:
-        // one conflict-free store.  It loads a unit's 16 scales of each row up
-        // to kDepth units ahead into registers.
-        const int group = warp - kMxFeedWarp0 - 1;  // -1: weights
-        const int kblocks = p.k / kMx4Block;
-        // load side: segment, unit and rows of the next step
-        int fseg = 0, fkb = 0, fend = 0;
-        const uint8_t *from = nullptr;  // scales of row `lane`
-        int have = 0;                   // rows from there on that exist
-        auto enter = [&]() {
-            if (fseg < sched.segs) {
-                const MxSeg g = mx_seg(sched, fseg);
-                const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
-                fkb = g.k0;
-                fend = g.k1;
-                const int ch = (int)rank * kMxBM + lane;
-                const int64_t left = group < 0 ? (int64_t)(p.n - w.ch - ch) : w.row_end - w.row - 128 * group - lane;
-                have = left < 0 ? 0 : (left < 128 ? (int)left : 128);
-                from = group < 0 ? p.ws + (w.wrow + ch) * p.stride : p.xs + (w.row + 128 * group + lane) * p.stride;
-            }
-        };
-        enter();
-        const int most = group < 0 ? kMxBM : TN - 128 * group;  // rows of the tile
-        auto fetch = [&](uint4 (&q)[4]) {
-            if (fseg >= sched.segs)
-                return;
-            const uint8_t *src = from + (int64_t)fkb * 16;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                q[j] = 32 * j < have && 32 * j + lane < most ? *reinterpret_cast<const uint4 *>(src + (int64_t)(32 * j) * p.stride)
-                                                             : make_uint4(0u, 0u, 0u, 0u);
-            if (++fkb == fend) {
-                ++fseg;
-                enter();
-            }
-        };
-        uint4 q[S::kDepth][4];
-#pragma unroll
-        for (int d = 0; d < S::kDepth; ++d)
-            fetch(q[d]);
-        int s = 0, seg = 0, kb = 0, end = 0, wrow = 0, xrow = 0;
-        auto next = [&]() {
-            if (seg < sched.segs) {
-                const MxSeg g = mx_seg(sched, seg);
-                kb = g.k0;
-                end = g.k1;
-                if (group < 0) {
-                    const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
-                    wrow = (int)w.wrow + (int)rank * kMxBM;
-                    xrow = (int)w.row + (int)rank * S::kBRows;
-                }
-            }
-        };
-        next();
-        int pre = 0;  // stages begun below
+    } else if (warp == kMxTmaWarp) {
+        // ---------------------------------------------------- producer ---
+        // Copies of the codes; both CTAs' bytes of a stage count on the
+        // leader's barrier.
+        int s = 0;
+        int pre = 0;  // stages begun early
         if (ahead) {
             // lane l begins stage l with this worker's unit l
             int seg0 = 0, unit = lane;
@@ -997,50 +953,157 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                     tma_load_2d<CG>(bring + lane * S::kBBytes + h * (S::kBBytes / 2), &xmap, col + h * (kMxBoxK / 2), row,
                                     smem_addr(&bars.full[lane]));
         }
-        uint32_t round = 0;  // of the ring
+        uint32_t round = 0;                  // of the ring
         uint32_t issued = (1u << pre) - 1u;  // stages that were ever filled: bits
+        bool ok = true;
+        for (int seg = 0; seg < sched.segs && ok; ++seg) {
+            const MxSeg g = mx_seg(sched, seg);
+            const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
+            const int wrow = (int)w.wrow + (int)rank * kMxBM, xrow = (int)w.row + (int)rank * S::kBRows;
+            for (int kb = g.k0; kb < g.k1; ++kb) {
+                if (pre > 0) {
+                    --pre;
+                } else {
+                    ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
+                    if (!ok)
+                        break;
+                    const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
+                    if (elect_one()) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + (FUSE ? 0 : S::kBBytes)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
+                            tma_load_2d<CG>(aring + s * kMxABytes + h * (kMxABytes / 2), &wmap, col, wrow, bar);
+                            if constexpr (!FUSE)
+                                tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
+                        }
+                    }
+                    __syncwarp();
+                    issued |= 1u << s;
+                }
+                if (++s == ST) {
+                    s = 0;
+                    ++round;
+                }
+            }
+        }
+        // copies in flight end before the CTA does (the second CTA of a pair
+        // leaves after the first, at the closing barrier).  Stages from s on
+        // were last filled in the round before this one (in round 0: early).
+        // If arrivals are missing, the limit that the first wait runs out of is
+        // long enough for all of them.
+        if (rank == 0) {
+            bool landed = true;
+            for (int j = 0; j < ST && landed; ++j) {
+                const int st = s + j < ST ? s + j : s + j - ST;
+                const uint32_t filled = st < s || round == 0 ? round : round - 1;
+                if (issued >> st & 1u)
+                    landed = warp_wait_uniform(&bars.full[st], filled & 1u, kDefaultWaitNs);
+            }
+            ok = ok && landed;
+        }
+        if (!ok && lane == 0)
+            record_timeout(p.status);
+    } else if (warp < kMxEpiWarp0) {
+        // ------------------------------------------------------ scales ---
+        // Lane l of the first warp owns the weights' rows l, l + 32, l + 64 and
+        // l + 96, of the second the tokens' (of the first 128).  Their scales of
+        // 128 columns are the 16 bytes at 16 l of the layout that the tensor
+        // core wants: one conflict-free store.  With 256 tokens each warp also
+        // takes two of the second 128's four rows, 8 bytes each.  A unit's 16
+        // scales of each row are loaded up to kDepth units ahead.  (The warp
+        // that issues the copies does nothing else: with a share of this work,
+        // 1400 cycles a unit, it was what the MMAs waited for.)
+        constexpr int NR = S::kScaleRows;
+        const int half = warp - kMxScaleWarp0;  // 0: weights
+        const int kblocks = p.k / kMx4Block;
+        // load side: segment, unit and rows of the next step
+        int fseg = 0, fkb = 0, fend = 0;
+        const uint8_t *from = nullptr, *from2 = nullptr;  // scales of rows `lane` and 128 + 64 half + lane
+        int have = 0, have2 = 0;                          // rows from there on that exist
+        auto enter = [&]() {
+            if (fseg < sched.segs) {
+                const MxSeg g = mx_seg(sched, fseg);
+                const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
+                fkb = g.k0;
+                fend = g.k1;
+                const int64_t tokens = w.row_end - w.row < TN ? w.row_end - w.row : TN;
+                const int ch = w.ch + (int)rank * kMxBM;
+                have = (half ? (int)tokens : p.n - ch) - lane;
+                from = half ? p.xs + (w.row + lane) * p.stride : p.ws + (w.wrow + (ch - w.ch) + lane) * p.stride;
+                if constexpr (NR > 4) {
+                    have2 = (int)tokens - 128 - 64 * half - lane;
+                    from2 = p.xs + (w.row + 128 + 64 * half + lane) * p.stride;
+                }
+            }
+        };
+        enter();
+        auto fetch = [&](uint4 (&q)[NR]) {
+            if (fseg >= sched.segs)
+                return;
+            const int64_t col = (int64_t)fkb * 16, hop = (int64_t)32 * p.stride;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = 32 * j < have ? *reinterpret_cast<const uint4 *>(from + col + j * hop) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 4; j < NR; ++j)
+                q[j] = 32 * (j - 4) < have2 ? *reinterpret_cast<const uint4 *>(from2 + col + (j - 4) * hop)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+            if (++fkb == fend) {
+                ++fseg;
+                enter();
+            }
+        };
+        uint4 q[S::kDepth][NR];
+#pragma unroll
+        for (int d = 0; d < S::kDepth; ++d)
+            fetch(q[d]);
+        int s = 0, seg = 0, kb = 0, end = 0;
+        auto next = [&]() {
+            if (seg < sched.segs) {
+                const MxSeg g = mx_seg(sched, seg);
+                kb = g.k0;
+                end = g.k1;
+            }
+        };
+        next();
+        uint32_t par = 1;
         bool ok = true;
         while (seg < sched.segs && ok) {
 #pragma unroll
             for (int d = 0; d < S::kDepth; ++d) {
                 if (seg < sched.segs && ok) {
-                    ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
+                    ok = warp_wait_uniform(&bars.empty[s], par, p.wait_ns);
                     if (ok) {
-                        if (pre > 0) {
-                            --pre;
-                        } else if (group < 0) {
-                            const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
-                            if (elect_one()) {
-                                if (rank == 0)
-                                    mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + (FUSE ? 0 : S::kBBytes)));
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
-                                    tma_load_2d<CG>(aring + s * kMxABytes + h * (kMxABytes / 2), &wmap, col, wrow, bar);
-                                    if constexpr (!FUSE)
-                                        tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        issued |= 1u << s;
-                        unsigned char *sc = scales + s * S::kScaleBytes + lane * 16 + (group < 0 ? 0 : 2048 + 512 * group);
-                        const int step = group < 0 ? 512 : 512 * S::kBGroups;
+                        unsigned char *sc = scales + s * S::kScaleBytes + lane * 16;
+                        unsigned char *main = sc + (half ? 2048 : 0);
+                        const int step = half ? 512 * S::kBGroups : 512;
                         const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
-                        uint32_t keep[4];
+                        uint32_t v[4][NR];                                    // [128 columns][row]
+#pragma unroll
+                        for (int j = 0; j < NR; ++j) {
+                            v[0][j] = q[d][j].x;
+                            v[1][j] = q[d][j].y;
+                            v[2][j] = q[d][j].z;
+                            v[3][j] = q[d][j].w;
+                        }
+                        if (left < kMxBK / kMx4Block) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int n4 = left - 4 * c;
+                                const uint32_t keep = n4 >= 4 ? 0xffffffffu : (n4 <= 0 ? 0u : (1u << (8 * n4)) - 1u);
+#pragma unroll
+                                for (int j = 0; j < NR; ++j)
+                                    v[c][j] &= keep;
+                            }
+                        }
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const int n4 = left - 4 * c;
-                            keep[c] = n4 >= 4 ? 0xffffffffu : (n4 <= 0 ? 0u : (1u << (8 * n4)) - 1u);
+                            *reinterpret_cast<uint4 *>(main + c * step) = make_uint4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                            if constexpr (NR > 4)
+                                *reinterpret_cast<uint2 *>(sc + 2048 + 512 * (2 * c + 1) + 8 * half) = make_uint2(v[c][4], v[c][5]);
                         }
-                        const uint4 *v = q[d];
-                        *reinterpret_cast<uint4 *>(sc) = make_uint4(v[0].x & keep[0], v[1].x & keep[0], v[2].x & keep[0], v[3].x & keep[0]);
-                        *reinterpret_cast<uint4 *>(sc + step) =
-                            make_uint4(v[0].y & keep[1], v[1].y & keep[1], v[2].y & keep[1], v[3].y & keep[1]);
-                        *reinterpret_cast<uint4 *>(sc + 2 * step) =
-                            make_uint4(v[0].z & keep[2], v[1].z & keep[2], v[2].z & keep[2], v[3].z & keep[2]);
-                        *reinterpret_cast<uint4 *>(sc + 3 * step) =
-                            make_uint4(v[0].w & keep[3], v[1].w & keep[3], v[2].w & keep[3], v[3].w & keep[3]);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -1051,7 +1114,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                         }
                         if (++s == ST) {
                             s = 0;
-                            ++round;
+                            par ^= 1u;
                         }
                         if (++kb == end) {
                             ++seg;
@@ -1066,21 +1129,6 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
                     }
                 }
             }
-        }
-        // copies in flight end before the CTA does (the second CTA of a pair
-        // leaves after the first, at the closing barrier).  Stages from s on
-        // were last filled in the round before this one (in round 0: early).
-        // If arrivals are missing, the limit that the first wait runs out of is
-        // long enough for all of them.
-        if (group < 0 && rank == 0) {
-            bool landed = true;
-            for (int j = 0; j < ST && landed; ++j) {
-                const int st = s + j < ST ? s + j : s + j - ST;
-                const uint32_t filled = st < s || round == 0 ? round : round - 1;
-                if (issued >> st & 1u)
-                    landed = warp_wait_uniform(&bars.full[st], filled & 1u, kDefaultWaitNs);
-            }
-            ok = ok && landed;
         }
         if (!ok && lane == 0)
             record_timeout(p.status);
