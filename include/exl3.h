@@ -390,14 +390,14 @@ exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, voi
 
 /*
  * exl3_mx4_matmul -- y = x . w^T for 4-bit x (m rows) and w (n rows), any m
- * and n, fp32 accumulation, y m x n fp16 or bf16 (row-major, one rounding).
+ * and n, fp32 accumulation, y m x n fp16, bf16 or fp32 (row-major; one rounding).
  * Few rows are bound by w's bytes, many by the tensor cores; the kernel
  * splits the work evenly over the SMs and adds split sums in a fixed order,
  * so results are deterministic.  `workspace` as for exl3_gemm (zero-filled
  * once; one workspace serves these calls and the calls above in turn), at
  * least exl3_mx4_matmul_workspace_size bytes (a size that depends on the
  * current device's SM count).  EXL3_ERR_UNSUPPORTED above 2^31 units of
- * 128 channels x a token tile x 256 columns.
+ * 128 channels x a token tile x 512 columns.
  */
 size_t exl3_mx4_matmul_workspace_size(int64_t m, int64_t k, int64_t n);
 exl3_status exl3_mx4_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, void *y,
@@ -420,7 +420,8 @@ exl3_status exl3_mx4_linear(const void *x, int dtype, const void *signs, int rot
  *   offsets  int32 [experts + 1] in DEVICE memory (exl3_moe_sort's): the host
  *            never learns the experts' row counts.  They must not decrease;
  *            values outside [0, rows] are taken to its ends.
- *   xc, xs   rows x k; wc, ws  experts x n x k; y  rows x n fp16 or bf16.
+ *   xc, xs   rows x k; wc, ws  experts x n x k; y  rows x n, fp32 where
+ *            exl3_moe_combine then rounds the weighted sum once.
  *            Rows of y from offsets[experts] on keep what they hold.
  *   experts  1 .. 512 (experts * n <= 2^30).
  * Otherwise as exl3_mx4_matmul.
@@ -458,15 +459,17 @@ exl3_status exl3_moe_gather(const void *x, int dtype, const int32_t *positions, 
 /*
  * exl3_moe_combine -- rows back to their tokens:
  *   y[t] = sum over j of weights[t][j] ys[positions[t][j]],
- * for ys rows x h and y tokens x h of one type, weights fp32 [tokens][topk] or
- * NULL (all ones).  fp32 sums in the order of j, one rounding; choices whose
- * position lies outside [0, rows) add nothing (a token without any gets 0).
+ * for ys rows x h and y tokens x h of one type (fp32 ys: y of any), weights fp32
+ * [tokens][topk] or NULL (all ones).  fp32 sums in the order of j, one rounding;
+ * choices whose position lies outside [0, rows) add nothing (a token without any
+ * gets 0).
  */
 exl3_status exl3_moe_combine(const void *ys, int dtype, const int32_t *positions, const float *weights,
-                             int64_t tokens, int64_t topk, int64_t h, int64_t rows, void *y, void *stream);
+                             int64_t tokens, int64_t topk, int64_t h, int64_t rows, void *y, int y_dtype,
+                             void *stream);
 
 /*
- * exl3_moe_combine_grad -- the gradients of exl3_moe_combine:
+ * exl3_moe_combine_grad -- the gradients of exl3_moe_combine (dy in ys's type):
  *   dys[positions[t][j]] = weights[t][j] dy[t]   (rows that no position names
  *                                                 keep what they hold)
  *   dweights[t][j] = <dy[t], ys[positions[t][j]]> in fp32 (0 without a row).

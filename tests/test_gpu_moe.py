@@ -103,6 +103,12 @@ def test_gather_combine_and_gradients(dtype, tokens, topk, experts, h):
         mag = moe.combine(np.abs(host(ys)), pos, None if weights is None else np.abs(weights))
         assert np.all(np.abs(y - ref) <= half_step(dtype) * np.abs(ref) + topk * 2.0 ** -23 * mag + 2.0 ** -25)
 
+    if dtype == torch.float32:  # fp32 rows, the sum rounded once to 16 bits
+        for out in TYPES[:2]:
+            y = host(exl3.exl3_moe_combine(ys, p, weights=dev(w), dtype=out))
+            ref, mag = moe.combine(host(ys), pos, w), moe.combine(np.abs(host(ys)), pos, np.abs(w))
+            assert np.all(np.abs(y - ref) <= half_step(out) * np.abs(ref) + topk * 2.0 ** -23 * mag + 2.0 ** -25)
+
     dy = torch.from_numpy(rng.standard_normal((tokens, h))).to(dtype).cuda()
     for weights in (w, None):
         dys, dw = exl3.exl3_moe_combine_grad(dy, ys, p, None if weights is None else dev(weights), dys=fill.clone())

@@ -217,7 +217,7 @@ def test_product_exact_with_equal_scales(m, k, n):
     x, w = operand(rng, m, k), operand(rng, n, k)
     ref = mx4.values(*x) @ mx4.values(*w).T
     assert np.abs(ref).max() < 60000
-    for dtype in (torch.float16, torch.bfloat16):
+    for dtype in TYPES:
         assert torch.equal(product(x, w, dtype).cpu(), torch.from_numpy(ref).to(dtype))
     if m * n > 1 << 20:  # the same on pairs of CTAs or not: bit for bit on every call
         assert torch.equal(product(x, w, torch.float16), product(x, w, torch.float16))
@@ -235,6 +235,7 @@ def test_product_with_scales(m, k, n):
     assert np.abs(ref).max() < 60000
     # 2^-25: half a step of the smallest fp16 values
     assert np.all(np.abs(y - ref) <= 2.0 ** -11 * np.abs(ref) + k * 2.0 ** -23 * mag + 2.0 ** -25)
+    assert np.all(np.abs(host(product(x, w, torch.float32)) - ref) <= k * 2.0 ** -23 * mag)
 
 
 def test_product_scales_of_single_blocks():
@@ -409,6 +410,9 @@ def test_expert_layer():
     xc, xs = exl3.exl3_mx4_quantize(dev(x), signs=dev(signs), rotate=True, positions=pos, out_rows=rows)
     ys = exl3.exl3_mx4_matmul_experts(xc, xs, offsets, wc.view(experts, n, -1), wsc.view(experts, n, -1), workspace=ws)
     y = host(exl3.exl3_moe_combine(ys, pos, weights=dev(gate)))
+    ys32 = exl3.exl3_mx4_matmul_experts(xc, xs, offsets, wc.view(experts, n, -1), wsc.view(experts, n, -1),
+                                        dtype=torch.float32, workspace=ws)
+    once = host(exl3.exl3_moe_combine(ys32, pos, weights=dev(gate), dtype=torch.float16))
     xv = mx4.values(*mx4.quantize(mx4.rotate(x, signs)))
     wv = mx4.values(*mx4.quantize(mx4.rotate(wm, signs))).reshape(experts, n, k)
     ref, mag = np.zeros((tokens, n)), np.zeros((tokens, n))
@@ -419,6 +423,8 @@ def test_expert_layer():
                 mag[t] += gate[t, j] * (np.abs(wv[ids[t, j]]) @ np.abs(xv[t]))
     # two roundings to fp16 (an expert's output, the sum), fp32 sums of k and topk terms
     assert np.all(np.abs(y - ref) <= (2 * 2.0 ** -11 + (k + topk) * 2.0 ** -23) * mag + 2.0 ** -24)
+    # fp32 between the two calls: one rounding
+    assert np.all(np.abs(once - ref) <= 2.0 ** -11 * np.abs(ref) + (k + topk) * 2.0 ** -23 * mag + 2.0 ** -25)
     assert not y[5].any()
 
 
@@ -523,8 +529,10 @@ def test_no_write_outside(m, k, n):
     off = dev(np.array([0, m // 2, m], dtype=np.int32))
     half = n // 2
     y3 = Guarded((m, half), torch.bfloat16)
+    y4 = Guarded((m, n), torch.float32)
+    exl3.exl3_mx4_matmul(codes.view, scales.view, wc, wsc, y=y4.view, workspace=ws.view)
     ws3 = Guarded((exl3.exl3_mx4_matmul_experts_workspace_size(m, k, half, 2),), torch.uint8, zero=True)
     exl3.exl3_mx4_matmul_experts(codes.view, scales.view, off, wc.view(2, half, -1), wsc.view(2, half, -1), y=y3.view,
                                  workspace=ws3.view)
-    assert all(g.intact() for g in (codes, scales, back, y, ws, ws2, y2, y3, ws3))
+    assert all(g.intact() for g in (codes, scales, back, y, ws, ws2, y2, y3, ws3, y4))
     assert torch.equal(y.view, y2.view)

@@ -45,7 +45,7 @@ def test_no_rows_is_no_work():
     assert lib.exl3_mx4_matmul_experts(None, None, None, B, C, None, 0, 0, 64, 8, 2, None, 0, None) == OK
     assert lib.exl3_moe_gather(None, 0, None, 0, 2, 8, 4, None, None) == OK
     assert lib.exl3_moe_gather(A, 0, B, 2, 2, 8, 0, None, None) == OK
-    assert lib.exl3_moe_combine(A, 0, None, None, 0, 2, 8, 4, None, None) == OK
+    assert lib.exl3_moe_combine(A, 0, None, None, 0, 2, 8, 4, None, 0, None) == OK
     assert lib.exl3_moe_combine_grad(None, A, 0, None, None, 0, 2, 8, 4, B, C, None) == OK
 
 
@@ -61,7 +61,7 @@ def matmul(xc=A, xs=B, wc=C, ws=D, y=E, dtype=0, m=4, k=256, n=64, space=F, nb=B
     return exl3.load().exl3_mx4_matmul(xc, xs, wc, ws, y, dtype, m, k, n, space, nb, None)
 
 
-SIZES = [dict(m=-1), dict(m=(1 << 30) + 1), dict(k=0), dict(k=100), dict(n=0), dict(n=(1 << 24) + 1), dict(dtype=2),
+SIZES = [dict(m=-1), dict(m=(1 << 30) + 1), dict(k=0), dict(k=100), dict(n=0), dict(n=(1 << 24) + 1), dict(dtype=3),
          dict(dtype=9)]
 
 
@@ -82,7 +82,7 @@ def test_matmul_workspace():
     assert exl3.exl3_mx4_matmul_experts_workspace_size(4, 256, 64, 513) == 0
 
 
-@pytest.mark.parametrize("bad", SIZES + [dict(x=None), dict(x=MIS), dict(signs=G + 8), dict(wc=None), dict(ws=None),
+@pytest.mark.parametrize("bad", SIZES + [dict(dtype=2), dict(x=None), dict(x=MIS), dict(signs=G + 8), dict(wc=None), dict(ws=None),
                                          dict(y=None), dict(y=A), dict(y=C), dict(rotate=1, k=96)])
 def test_linear_refusals(bad):
     a = dict(x=A, dtype=0, signs=None, rotate=0, wc=C, ws=D, y=E, m=4, k=256, n=64, space=F, nb=BIG)
@@ -127,9 +127,10 @@ def test_gather_refusals(bad):
     assert exl3.load().exl3_moe_gather(*a.values(), None) == INV
 
 
-@pytest.mark.parametrize("bad", ROUTE + [dict(ys=None), dict(w=D + 4), dict(y=None), dict(y=A), dict(y=B), dict(y=D)])
+@pytest.mark.parametrize("bad", ROUTE + [dict(ys=None), dict(w=D + 4), dict(y=None), dict(y=A), dict(y=B), dict(y=D), dict(ydt=1), dict(ydt=2),
+                                         dict(dtype=2, ydt=3)])
 def test_combine_refusals(bad):
-    a = dict(ys=A, dtype=0, pos=B, w=D, tokens=4, topk=2, h=16, rows=8, y=C)
+    a = dict(ys=A, dtype=0, pos=B, w=D, tokens=4, topk=2, h=16, rows=8, y=C, ydt=0)
     a.update(bad)
     assert exl3.load().exl3_moe_combine(*a.values(), None) == INV
 

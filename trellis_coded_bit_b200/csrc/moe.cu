@@ -200,10 +200,21 @@ constexpr int kCombineThreads = 128;
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const float (&v)[V])
 {
-    if constexpr (V == 1)
+    if constexpr (V == 1) {
         *p = from_f32<T>(v[0]);
-    else
+    } else if constexpr (V == Vec<T>::N) {
         *reinterpret_cast<uint4 *>(p) = pack16<T>(v);
+    } else {
+        // 4 fp32 sums to 8 bytes
+        static_assert(V == 4 && sizeof(T) == 2, "narrowing store");
+        T e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            e[i] = from_f32<T>(v[i]);
+        uint2 raw;
+        memcpy(&raw, e, 8);
+        *reinterpret_cast<uint2 *>(p) = raw;
+    }
 }
 
 // A row number read from the caller's tensor: -1 (no row) unless it is one of
@@ -237,10 +248,10 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const U *__restrict__ x
 }
 
 // Bound by the rows' bytes: 8192 tokens x 8 rows of 8 KB in 97 us, 6.2 TB/s.
-template <typename T, int V>
+template <typename T, typename O, int V>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const T *__restrict__ ys, const int32_t *__restrict__ positions,
                                                           const float *__restrict__ weights, int64_t tokens, int topk,
-                                                          int64_t h, int64_t rows, T *__restrict__ y)
+                                                          int64_t h, int64_t rows, O *__restrict__ y)
 {
     grid_dep_wait();
     const int64_t cols = h / V;
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const T *_
                             acc[i] = fmaf(w[j], v[i], acc[i]);
                     }
             }
-            store_vec<T, V>(y + t * h + c * V, acc);
+            store_vec<O, V>(y + t * h + c * V, acc);
         }
     }
 }
@@ -371,14 +382,23 @@ static bool valid_route(int64_t tokens, int64_t topk, int64_t h, int64_t rows, i
            h <= (int64_t)1 << 22 && rows >= 0 && rows <= (int64_t)1 << 31;
 }
 
-template <typename T, int V>
+template <typename T, typename O, int V>
+static exl3_status launch_combine_v(const void *ys, const int32_t *positions, const float *weights, int64_t tokens,
+                                    int64_t topk, int64_t h, int64_t rows, void *y, cudaStream_t s)
+{
+    if (launch_kernel(moe_combine_kernel<T, O, V>, row_grid(tokens, h / V, kCombineThreads), dim3(kCombineThreads), 0, s, (const T *)ys, positions,
+                      weights, tokens, (int)topk, h, rows, (O *)y) != cudaSuccess)
+        return EXL3_ERR_CUDA;
+    return launch_status();
+}
+
+template <typename T, typename O>
 static exl3_status launch_combine(const void *ys, const int32_t *positions, const float *weights, int64_t tokens,
                                   int64_t topk, int64_t h, int64_t rows, void *y, cudaStream_t s)
 {
-    if (launch_kernel(moe_combine_kernel<T, V>, row_grid(tokens, h / V, kCombineThreads), dim3(kCombineThreads), 0, s, (const T *)ys, positions,
-                      weights, tokens, (int)topk, h, rows, (T *)y) != cudaSuccess)
-        return EXL3_ERR_CUDA;
-    return launch_status();
+    return h * sizeof(T) % 16 == 0
+               ? launch_combine_v<T, O, Vec<T>::N>(ys, positions, weights, tokens, topk, h, rows, y, s)
+               : launch_combine_v<T, O, 1>(ys, positions, weights, tokens, topk, h, rows, y, s);
 }
 
 template <typename T, int V>
@@ -470,32 +490,30 @@ extern "C" exl3_status exl3_moe_gather(const void *x, int dtype, const int32_t *
 }
 
 extern "C" exl3_status exl3_moe_combine(const void *ys, int dtype, const int32_t *positions, const float *weights,
-                                        int64_t tokens, int64_t topk, int64_t h, int64_t rows, void *y, void *stream)
+                                        int64_t tokens, int64_t topk, int64_t h, int64_t rows, void *y, int y_dtype,
+                                        void *stream)
 {
     using namespace exl3;
-    if (!valid_route(tokens, topk, h, rows, dtype))
+    if (!valid_route(tokens, topk, h, rows, dtype) || !valid_dtype(y_dtype) || (y_dtype != dtype && dtype != EXL3_F32))
         return EXL3_ERR_INVALID_ARG;
     if (tokens == 0)
         return EXL3_OK;
     if ((rows && (!ys || !aligned16(ys))) || !positions || !y || !aligned16(positions) || !aligned16(y) ||
         (weights && !aligned16(weights)))
         return EXL3_ERR_INVALID_ARG;
-    const size_t row = (size_t)h * dtype_bytes(dtype), yb = (size_t)tokens * row, cb = (size_t)(tokens * topk) * 4;
+    const size_t row = (size_t)h * dtype_bytes(dtype), yb = (size_t)(tokens * h) * dtype_bytes(y_dtype), cb = (size_t)(tokens * topk) * 4;
     if ((rows && ranges_overlap(ys, (size_t)rows * row, y, yb)) || ranges_overlap(positions, cb, y, yb) ||
         (weights && ranges_overlap(weights, cb, y, yb)))
         return EXL3_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
-    const bool vec = row % 16 == 0;
-    switch (dtype) {
-    case EXL3_F16:
-        return vec ? launch_combine<__half, 8>(ys, positions, weights, tokens, topk, h, rows, y, s)
-                   : launch_combine<__half, 1>(ys, positions, weights, tokens, topk, h, rows, y, s);
-    case EXL3_BF16:
-        return vec ? launch_combine<__nv_bfloat16, 8>(ys, positions, weights, tokens, topk, h, rows, y, s)
-                   : launch_combine<__nv_bfloat16, 1>(ys, positions, weights, tokens, topk, h, rows, y, s);
-    default:
-        return vec ? launch_combine<float, 4>(ys, positions, weights, tokens, topk, h, rows, y, s)
-                   : launch_combine<float, 1>(ys, positions, weights, tokens, topk, h, rows, y, s);
+    if (dtype == EXL3_F16)
+        return launch_combine<__half, __half>(ys, positions, weights, tokens, topk, h, rows, y, s);
+    if (dtype == EXL3_BF16)
+        return launch_combine<__nv_bfloat16, __nv_bfloat16>(ys, positions, weights, tokens, topk, h, rows, y, s);
+    switch (y_dtype) {
+    case EXL3_F16: return launch_combine<float, __half>(ys, positions, weights, tokens, topk, h, rows, y, s);
+    case EXL3_BF16: return launch_combine<float, __nv_bfloat16>(ys, positions, weights, tokens, topk, h, rows, y, s);
+    default: return launch_combine<float, float>(ys, positions, weights, tokens, topk, h, rows, y, s);
     }
 }
 

@@ -491,6 +491,20 @@ __device__ __forceinline__ void mx_epi_sync()
     asm volatile("bar.sync 1, %0;\n" ::"n"(32 * MxTile<TN, CG>::kEpiWarps) : "memory");
 }
 
+// Hands accumulator `acc` back to the MMA issuer, one arrival a warp.
+template <int CG>
+__device__ __forceinline__ void mx_release(MxBars &bars, int acc)
+{
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        if constexpr (CG == 1)
+            mbar_arrive(&bars.acc_empty[acc]);
+        else
+            mbar_arrive_leader(&bars.acc_empty[acc]);
+    }
+}
+
 // Segment `seg` of this worker.  Returns false if its accumulators never came
 // (the caller stops).
 template <typename T, int TN, int CG>
@@ -540,7 +554,28 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     const bool wide = (p.n & 7) == 0;
     T *const y = reinterpret_cast<T *>(p.y) + (w.row + c0) * p.n + ch;
 
-    if (whole) {
+    if constexpr (sizeof(T) == 4) {
+        // fp32: a warp's 32 channels of a token are 128 contiguous bytes as
+        // they come from TMEM
+        if (whole) {
+            constexpr int kStep = kCols % 32 == 0 ? 32 : 16;
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += kStep) {
+                uint32_t b[kStep];
+                if constexpr (kStep == 32)
+                    EXL3_TMEM_LD32(d + c, b);
+                else
+                    EXL3_TMEM_LD16(d + c, b);
+                if (c + kStep == kCols)
+                    mx_release<CG>(bars, acc);
+#pragma unroll
+                for (int i = 0; i < kStep; ++i)
+                    if (c + i < cols && lane < ch_left)
+                        y[(int64_t)(c + i) * p.n + lane] = __uint_as_float(b[i]);
+            }
+            return true;
+        }
+    } else if (whole) {
         // everything into registers (16 bits each), so that the MMA issuer
         // gets the accumulator back before the stores
         uint32_t v[kCols / 2];
@@ -563,14 +598,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                     v[c / 2 + i] = pack2<T>(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
             }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            if constexpr (CG == 1)
-                mbar_arrive(&bars.acc_empty[acc]);
-            else
-                mbar_arrive_leader(&bars.acc_empty[acc]);
-        }
+        mx_release<CG>(bars, acc);
         if (wide && cols == kCols && ch_left >= 32) {
             // Pairs: the stores are spread over about a third of the next tile's
             // main loop; in one burst they held up its scales' loads (4096 x 4096
@@ -664,24 +692,24 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
                     }
                 }
             }
-            uint32_t v[8];
+            if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = pack2<T>(s[2 * i], s[2 * i + 1]);
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < cols && lane < ch_left)
+                        y[(int64_t)(c + i) * p.n + lane] = s[i];
+            } else {
+                uint32_t v[8];
 #pragma unroll
-            for (int h = 0; h < 16; h += 8)
-                if (c + h < cols)
-                    mx_store8<T>(y + (int64_t)(c + h) * p.n, p.n, v + h / 2, cols - c - h, ch_left, wide);
+                for (int i = 0; i < 8; ++i)
+                    v[i] = pack2<T>(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+                for (int h = 0; h < 16; h += 8)
+                    if (c + h < cols)
+                        mx_store8<T>(y + (int64_t)(c + h) * p.n, p.n, v + h / 2, cols - c - h, ch_left, wide);
+            }
         }
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-        if constexpr (CG == 1)
-            mbar_arrive(&bars.acc_empty[acc]);
-        else
-            mbar_arrive_leader(&bars.acc_empty[acc]);
-    }
+    mx_release<CG>(bars, acc);
     return true;
 }
 
@@ -1264,8 +1292,9 @@ template <typename T>
 static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap,
                                   int workers, bool pdl, cudaStream_t s)
 {
-    if (p.x)
-        return launch_mx<T, 16, 1, true>(p, wmap, xmap, workers, pdl, s);
+    if constexpr (sizeof(T) == 2)
+        if (p.x)
+            return launch_mx<T, 16, 1, true>(p, wmap, xmap, workers, pdl, s);
     switch (tn) {
     case 16: return launch_mx<T, 16, 1>(p, wmap, xmap, workers, pdl, s);
     case 32: return launch_mx<T, 32, 1>(p, wmap, xmap, workers, pdl, s);
@@ -1278,14 +1307,14 @@ static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &
 static exl3_status check_mx(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, const void *y,
                             int dtype, int64_t m, int64_t k, int64_t n, int64_t experts)
 {
-    if (!valid_mx_sizes(m, k, n, experts) || (dtype != EXL3_F16 && dtype != EXL3_BF16))
+    if (!valid_mx_sizes(m, k, n, experts) || (dtype != EXL3_F16 && dtype != EXL3_BF16 && dtype != EXL3_F32))
         return EXL3_ERR_INVALID_ARG;
     if (m == 0)
         return EXL3_OK;
     if (!xc || !xs || !wc || !ws || !y || !aligned16(xc) || !aligned16(xs) || !aligned16(wc) || !aligned16(ws) ||
         !aligned16(y))
         return EXL3_ERR_INVALID_ARG;
-    const size_t st = (size_t)mx4_scale_stride(k), yb = (size_t)m * (size_t)n * 2;
+    const size_t st = (size_t)mx4_scale_stride(k), yb = (size_t)m * (size_t)n * (dtype == EXL3_F32 ? 4 : 2);
     const void *in[4] = {xc, xs, wc, ws};
     const size_t bytes[4] = {(size_t)m * (size_t)(k / 2), (size_t)m * st, (size_t)(experts * n) * (size_t)(k / 2),
                              (size_t)(experts * n) * st};
@@ -1333,8 +1362,11 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     const int64_t most = num_sms() / cg;
     const int workers = (int)(tiles * p.kb_count < most ? tiles * p.kb_count : most);
     pdl = pdl || (launch_flags() & EXL3_LAUNCH_PDL);
-    return dtype == EXL3_F16 ? launch_mx_tile<__half>(tn, p, wmap, xmap, workers, pdl, s)
-                             : launch_mx_tile<__nv_bfloat16>(tn, p, wmap, xmap, workers, pdl, s);
+    switch (dtype) {
+    case EXL3_F16: return launch_mx_tile<__half>(tn, p, wmap, xmap, workers, pdl, s);
+    case EXL3_BF16: return launch_mx_tile<__nv_bfloat16>(tn, p, wmap, xmap, workers, pdl, s);
+    default: return launch_mx_tile<float>(tn, p, wmap, xmap, workers, pdl, s);
+    }
 }
 
 // Workspace of exl3_mx4_linear: the matmul's, then the quantised activations.
@@ -1386,7 +1418,7 @@ extern "C" exl3_status exl3_mx4_matmul_experts(const uint8_t *xc, const uint8_t 
     if (st != EXL3_OK || rows == 0)
         return st;
     if (!offsets || !aligned16(offsets) ||
-        ranges_overlap(offsets, (size_t)(experts + 1) * 4, y, (size_t)rows * (size_t)n * 2))
+        ranges_overlap(offsets, (size_t)(experts + 1) * 4, y, (size_t)rows * (size_t)n * (dtype == EXL3_F32 ? 4 : 2)))
         return EXL3_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace) || workspace_bytes < mx_workspace(rows, n, experts))
         return EXL3_ERR_WORKSPACE;

@@ -125,7 +125,7 @@ def load(build_if_needed=True):
         lib.exl3_moe_sort_workspace_size.argtypes = [i64, i64, i64]
         lib.exl3_moe_sort.argtypes = [vp, i64, i64, i64, vp, vp, vp, sz, vp]
         lib.exl3_moe_gather.argtypes = [vp, ci, vp, i64, i64, i64, i64, vp, vp]
-        lib.exl3_moe_combine.argtypes = [vp, ci, vp, vp, i64, i64, i64, i64, vp, vp]
+        lib.exl3_moe_combine.argtypes = [vp, ci, vp, vp, i64, i64, i64, i64, vp, ci, vp]
         lib.exl3_moe_combine_grad.argtypes = [vp, vp, ci, vp, vp, i64, i64, i64, i64, vp, vp, vp]
         for name in ("mx4_matmul", "mx4_linear", "mx4_matmul_experts", "moe_sort"):
             getattr(lib, "exl3_%s_workspace_size" % name).restype = sz
@@ -564,7 +564,7 @@ def exl3_mx4_matmul_workspace_size(m, k, n):
 
 
 def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None, stream=None):
-    """y = x . w^T of two 4-bit matrices (m rows and n rows of k), fp16 or bf16."""
+    """y = x . w^T of two 4-bit matrices (m rows and n rows of k), fp16, bf16 or fp32."""
     (m,), k = _mx4_operand(xc, xs, 1, "x")
     (n,), kw = _mx4_operand(wc, ws, 1, "w")
     if kw != k:
@@ -573,7 +573,7 @@ def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None,
         y = xc.new_empty((m, n), dtype=dtype)
     else:
         _shape(y, (m, n), "y")
-    device, dt = _device(y, "y", _HALF_TYPES)
+    device, dt = _device(y, "y", DTYPES)
     _call("exl3_mx4_matmul", device, stream, _arg(xc, torch.uint8, "x codes", device),
           _arg(xs, torch.uint8, "x scales", device), _arg(wc, torch.uint8, "w codes", device),
           _arg(ws, torch.uint8, "w scales", device), _arg(y, y.dtype, "y", device), dt, m, k, n,
@@ -624,7 +624,7 @@ def exl3_mx4_matmul_experts(xc, xs, offsets, wc, ws, dtype=torch.float16, y=None
         y = xc.new_empty((rows, n), dtype=dtype)
     else:
         _shape(y, (rows, n), "y")
-    device, dt = _device(y, "y", _HALF_TYPES)
+    device, dt = _device(y, "y", DTYPES)
     _call("exl3_mx4_matmul_experts", device, stream, _arg(xc, torch.uint8, "x codes", device),
           _arg(xs, torch.uint8, "x scales", device), _arg(offsets, torch.int32, "offsets", device),
           _arg(wc, torch.uint8, "w codes", device), _arg(ws, torch.uint8, "w scales", device),
@@ -682,8 +682,9 @@ def exl3_moe_gather(x, positions, out=None, out_rows=None, stream=None):
     return out
 
 
-def exl3_moe_combine(ys, positions, weights=None, y=None, stream=None):
-    """y[t] = sum over j of weights[t, j] ys[positions[t, j]] (weights fp32, None: ones)."""
+def exl3_moe_combine(ys, positions, weights=None, dtype=None, y=None, stream=None):
+    """y[t] = sum over j of weights[t, j] ys[positions[t, j]] (weights fp32,
+    None: ones); y has ys's type, or with fp32 ys the one of `dtype`."""
     if ys.dim() != 2:
         raise ValueError("ys must be rows x h")
     rows, h = ys.shape
@@ -693,13 +694,15 @@ def exl3_moe_combine(ys, positions, weights=None, y=None, stream=None):
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
     if y is None:
-        y = ys.new_empty((tokens, h), dtype=ys.dtype)
+        y = ys.new_empty((tokens, h), dtype=ys.dtype if dtype is None else dtype)
     else:
         _shape(y, (tokens, h), "y")
+    if y.dtype not in DTYPES or (y.dtype != ys.dtype and ys.dtype != torch.float32):
+        raise TypeError("y must be %s, got %s" % (ys.dtype, y.dtype))
     _call("exl3_moe_combine", device, stream, _arg(ys, ys.dtype, "ys", device), dt,
           _arg(positions, torch.int32, "positions", device),
           None if weights is None else _arg(weights, torch.float32, "weights", device), tokens, topk, h, rows,
-          _arg(y, ys.dtype, "y", device))
+          _arg(y, y.dtype, "y", device), DTYPES[y.dtype])
     return y
 
 
