@@ -326,8 +326,10 @@ def _run_own(s):
         rows = case["tokens"] * case["topk"]
         offsets, positions = exl3.exl3_moe_sort(s["ids"], case["experts"], workspace=s["workspace"])
         xc, xs = exl3.exl3_mx4_quantize(s["x"], signs=s["signs"], rotate=True, positions=positions, out_rows=rows)
-        ys = exl3.exl3_mx4_matmul_experts(xc, xs, offsets, s["w"], s["ws"], dtype=dtype, workspace=s["workspace"])
-        return {"offsets": offsets, "positions": positions, "y": exl3.exl3_moe_combine(ys, positions, weights=s["weights"])}
+        # fp32 rows, so that the weighted sum is rounded once
+        ys = exl3.exl3_mx4_matmul_experts(xc, xs, offsets, s["w"], s["ws"], dtype=torch.float32, workspace=s["workspace"])
+        y = exl3.exl3_moe_combine(ys, positions, weights=s["weights"], dtype=dtype)
+        return {"offsets": offsets, "positions": positions, "y": y}
     if op == "route":
         offsets, positions = exl3.exl3_moe_sort(s["ids"], case["experts"], workspace=s["workspace"])
         xs = exl3.exl3_moe_gather(s["x"], positions, out=s["out"])
