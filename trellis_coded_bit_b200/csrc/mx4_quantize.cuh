@@ -194,7 +194,7 @@ __device__ __forceinline__ float sticky32(double v)
 }
 
 // A block in fp64, read again (x, signs: the thread's 32 columns).  A call of
-// its own: about one warp in 70 of normal data comes here.
+// its own: about one warp in 30 of normal data comes here.
 template <typename T>
 __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *signs, int *byte)
 {

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of the EXL3 B200 C ABI (include/exl3.h).
+"""Thin ctypes binding of the EXL3 B200 C ABI (include/exl3.h): layers of trellis
+weights, 4-bit microscaled matrices (exl3_mx4_*) and expert routing (exl3_moe_*).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libexl3_b200.so.  PyTorch supplies device memory and streams.
