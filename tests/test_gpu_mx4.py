@@ -206,7 +206,9 @@ SHAPES = [(1, 32, 1), (1, 256, 128), (1, 64, 5), (2, 96, 129), (16, 128, 128), (
           (200, 4096, 128), (256, 256, 256), (257, 160, 131), (300, 4000, 1000), (1, 4096, 4096), (8, 14336, 512),
           (513, 512, 640), (40, 8192, 77),
           # pairs of CTAs: whole tiles, split tiles, odd rows and channels
-          (520, 1536, 13001), (1100, 544, 9100), (2100, 96, 4360)]
+          (520, 1536, 13001), (1100, 544, 9100), (2100, 96, 4360), (40000, 64, 272),
+          # a long sum
+          (3, 262144, 40)]
 
 
 @pytest.mark.parametrize("m,k,n", SHAPES)
@@ -390,6 +392,67 @@ def test_experts_offsets_outside_the_rows():
     xv, wv = mx4.values(*x), mx4.values(*w).reshape(3, n, k)
     ref = np.concatenate([xv[:4] @ wv[0].T, xv[4:] @ wv[1].T])
     assert torch.equal(y.cpu(), torch.from_numpy(ref).half())
+
+
+def test_more_than_32_bits_of_elements():
+    """Matrices whose element offsets pass 2^31: the last rows against the same rows alone."""
+    rows, k = 600000, 4096
+    x = torch.zeros((rows, k), dtype=torch.float16, device="cuda")
+    x[-3:] = torch.randn((3, k), device="cuda").half()
+    codes, scales = exl3.exl3_mx4_quantize(x, rotate=True)
+    c3, s3 = exl3.exl3_mx4_quantize(x[-3:].clone(), rotate=True)
+    assert torch.equal(codes[-3:], c3) and torch.equal(scales[-3:], s3) and not codes[:-3].any()
+    assert torch.equal(exl3.exl3_mx4_dequantize(codes, scales, out=x)[-3:], exl3.exl3_mx4_dequantize(c3, s3))
+    codes, scales = exl3.exl3_mx4_quantize(x)
+    assert torch.equal(codes[-3:], exl3.exl3_mx4_quantize(x[-3:].clone())[0])
+    del x, codes, scales
+    rng = np.random.default_rng(61)
+    m, n, k = 70000, 32768, 64
+    x, w = operand(rng, m, k), operand(rng, n, k)
+    y = product(x, w, torch.float16)
+    for r in (0, 65535, 65537, m - 1):
+        ref = mx4.values(x[0][r:r + 1], x[1][r:r + 1]) @ mx4.values(*w).T
+        assert torch.equal(y[r].cpu(), torch.from_numpy(ref[0]).half())
+
+
+def test_captured_expert_layer():
+    """The run of calls of an expert layer, captured once and replayed on other
+    tokens, choices and weights in the same buffers."""
+    rng = np.random.default_rng(23)
+    tokens, topk, experts, k, n = 300, 2, 8, 256, 264
+    wc, wsc = exl3.exl3_mx4_quantize(torch.from_numpy(rng.standard_normal((experts * n, k))).float().cuda(), rotate=True)
+    wc, wsc = wc.view(experts, n, -1), wsc.view(experts, n, -1)
+    x = torch.empty((tokens, k), dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty((tokens, topk), dtype=torch.int32, device="cuda")
+    gate = torch.empty((tokens, topk), device="cuda")
+    ws = exl3.new_workspace(max(exl3.exl3_moe_sort_workspace_size(tokens, topk, experts),
+                                exl3.exl3_mx4_matmul_experts_workspace_size(tokens * topk, k, n, experts)))
+
+    def layer():
+        offsets, pos = exl3.exl3_moe_sort(ids, experts, workspace=ws)
+        xc, xs = exl3.exl3_mx4_quantize(x, rotate=True, positions=pos, out_rows=tokens * topk)
+        ys = exl3.exl3_mx4_matmul_experts(xc, xs, offsets, wc, wsc, dtype=torch.float32, workspace=ws)
+        return exl3.exl3_moe_combine(ys, pos, weights=gate, dtype=torch.bfloat16)
+
+    def fill(seed, one=None):
+        r = np.random.default_rng(seed)
+        x.copy_(torch.from_numpy(r.standard_normal((tokens, k))))
+        chosen = r.integers(-1, experts, (tokens, topk)) if one is None else np.full((tokens, topk), one)
+        ids.copy_(torch.from_numpy(chosen.astype(np.int32)))
+        gate.copy_(torch.from_numpy(r.random((tokens, topk))))
+
+    fill(1)
+    layer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer()
+    for seed, one in ((2, None), (3, 7), (4, -1)):  # mixed, one expert takes all, none chosen
+        fill(seed, one)
+        graph.replay()
+        got = y.clone()
+        assert torch.equal(got, layer())
+        assert one != -1 or not got.any()
+    assert exl3.exl3_workspace_status(ws) == exl3.EXL3_OK
 
 
 def test_expert_layer():

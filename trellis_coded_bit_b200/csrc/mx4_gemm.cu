@@ -317,9 +317,9 @@ __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const MxTables &t
 //
 // Split tiles: `even` gives each tile floor or ceil(W / tiles) workers of its
 // own, so a worker has one segment and waits for one sum; otherwise the units
-// (tile, 256 columns) in order are cut into equal shares, and a worker may end
+// (tile, 512 columns) in order are cut into equal shares, and a worker may end
 // one tile and begin the next.  Even is taken where its longest segment is at
-// most one unit longer (4096 channels, k = 4096: 4 units either way).
+// most one unit longer (4096 channels, k = 4096: 2 units either way).
 struct MxSched {
     uint32_t worker, G, KB;
     uint32_t whole;      // whole tiles of each worker
@@ -538,6 +538,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     }
     // the epilogue warps agree, so that none is left at a barrier of the
     // others (only they write the flag, and only before this barrier)
+    __syncwarp();
     mx_epi_sync<TN, CG>();
     const bool stop = *epi_abort != 0;
     mx_epi_sync<TN, CG>();
@@ -649,6 +650,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
         bars.ticket = last;
         __threadfence();
     }
+    __syncwarp();
     mx_epi_sync<TN, CG>();
     if (bars.ticket) {
         // sums in segment order, this CTA's own from TMEM; kAhead segments'
@@ -1235,8 +1237,8 @@ static int mx_token_tile(int64_t rows, int64_t n, int64_t experts)
 // Workers that may share a tile of kb units: w of them take kb/w units each and
 // then w partial sums of TN x 128 per CTA to add, so w = sqrt(kb unit/partial).
 // A unit takes 1.1 us (256 tokens), 0.7 us (fewer), a partial written and read
-// 0.35 us and 0.012 us a token: 333 x 4000 x 10001 with 8 workers on each of 6
-// left-over tiles took 44 us, with 2 a half.
+// 0.35 us and 0.012 us a token.  (333 x 4000 x 10001 on pairs took 44 us with 8
+// workers on each of the 6 tiles left over, with 1 or 2 it took 32.)
 static uint32_t mx_most_workers(int tn, int kb)
 {
     const double unit = tn > 128 ? 1.1 : 0.7, partial = 0.35 + 0.012 * tn;
