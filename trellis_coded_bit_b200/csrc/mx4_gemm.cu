@@ -559,20 +559,27 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
         // fp32: a warp's 32 channels of a token are 128 contiguous bytes as
         // they come from TMEM
         if (whole) {
-            constexpr int kStep = kCols % 32 == 0 ? 32 : 16;
+            constexpr int kLoad = kCols % 32 == 0 ? 32 : 16, kStep = kCols % 64 == 0 ? 64 : kLoad;
 #pragma unroll 1
             for (int c = 0; c < kCols; c += kStep) {
-                uint32_t b[kStep];
-                if constexpr (kStep == 32)
-                    EXL3_TMEM_LD32(d + c, b);
-                else
-                    EXL3_TMEM_LD16(d + c, b);
+                float v[kStep];
+#pragma unroll
+                for (int h = 0; h < kStep; h += kLoad) {
+                    uint32_t b[kLoad];
+                    if constexpr (kLoad == 32)
+                        EXL3_TMEM_LD32(d + c + h, b);
+                    else
+                        EXL3_TMEM_LD16(d + c + h, b);
+#pragma unroll
+                    for (int i = 0; i < kLoad; ++i)
+                        v[h + i] = __uint_as_float(b[i]);
+                }
                 if (c + kStep == kCols)
                     mx_release<CG>(bars, acc);
 #pragma unroll
                 for (int i = 0; i < kStep; ++i)
                     if (c + i < cols && lane < ch_left)
-                        y[(int64_t)(c + i) * p.n + lane] = __uint_as_float(b[i]);
+                        y[(int64_t)(c + i) * p.n + lane] = v[i];
             }
             return true;
         }
