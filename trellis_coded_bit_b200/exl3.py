@@ -442,6 +442,16 @@ _HALF_TYPES = (torch.float16, torch.bfloat16)
 
 def _arg(t, dtype, name, device):
     """Address of a contiguous CUDA tensor of `dtype` on device number `device`."""
+    try:
+        # a device number belongs to a CUDA tensor: others have -1
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, name, device)
+
+
+def _refuse(t, dtype, name, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -451,20 +461,24 @@ def _arg(t, dtype, name, device):
     if t.get_device() != device:
         raise ValueError("tensors of one call must be on one device: %s is on %s, not cuda:%d"
                          % (name, t.device, device))
-    return t.data_ptr()
 
 
 def _device(t, name, types):
     """Device number and exl3_dtype of a call's first tensor."""
+    try:
+        if t.is_cuda and t.dtype in types:
+            return t.get_device(), DTYPES.get(t.dtype)
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype not in types:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in types), t.dtype))
-    return t.get_device(), DTYPES.get(t.dtype)
+    raise TypeError("%s is no tensor that this call can take" % name)
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s, is %s" % (name, " x ".join(str(s) for s in shape), tuple(t.shape)))
 
 
@@ -472,7 +486,7 @@ def _call(name, device, stream, *args):
     """Calls the library on `stream`, or on the current stream of `device`,
     with that device current."""
     fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
         status = fn(*args, s)
     else:
@@ -503,7 +517,7 @@ def _mx4_stride(k):
 
 def _mx4_operand(codes, scales, dims, what):
     """Checks a 4-bit operand's shapes; returns its leading dimensions and k."""
-    shape = tuple(codes.shape)
+    shape = codes.shape
     if len(shape) != dims + 1:
         raise ValueError("%s codes must have %d dimensions" % (what, dims + 1))
     k = shape[-1] * 2
