@@ -55,6 +55,7 @@ constexpr int kMxMmaWarp = 0, kMxTmaWarp = 1, kMxScaleWarp0 = 2, kMxEpiWarp0 = 4
 constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
 constexpr int kMxMaxExperts = 512;
 constexpr int kMxFuseRows = 2;                   // tokens that the product of a layer quantises itself
+constexpr int kMxQuantWarps = 4;                 // warps that quantise them
 constexpr size_t kMxSyncArea = 64 * 1024;
 // Shared memory of the experts' tables: each one's first tile and first row.
 constexpr int mx_table_bytes(int experts)
@@ -80,7 +81,9 @@ struct MxTile {
     static constexpr int kAccCols = TN < 32 ? 32 : TN;
     static constexpr int kEpiWarps = TN >= 128 ? 8 : 4;         // each: 32 lanes x kEpiCols columns
     static constexpr int kEpiCols = TN / (kEpiWarps / 4);
-    static constexpr int kThreads = 32 * (kMxEpiWarp0 + kEpiWarps);
+    static constexpr int kWarps = kMxEpiWarp0 + kEpiWarps;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kFuseThreads = kThreads + 32 * (kMxQuantWarps - 1);  // one takes a scale warp's place
     static constexpr int kSmem = 2048 + kStages * kStageBytes;
     static_assert(kAcc * kAccCols + kStages * kScaleCols <= 512, "TMEM columns");
 };
@@ -724,17 +727,20 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
 
 // --------------------------------------------------------- main kernel ---
 
-// FUSE: the tokens (kMxFuseRows at most) come as rows of T, and the warp that
-// would deal out their scales quantises them, codes and scales, straight into
-// the stage: 4 lanes a rotation, 16 a token and unit, so one pass of the warp a
-// unit.  Every CTA repeats it for its units; the weights' bytes still bound the
-// unit, and a launch and its 3 us are gone.
+// FUSE: the tokens (kMxFuseRows at most) come as rows of T, and kMxQuantWarps
+// warps in turn (one of them in the place of the warp that would deal out the
+// tokens' scales) quantise them, codes and scales, straight into the stage: 4
+// lanes a rotation, 16 a token and unit, so one pass of a warp a unit.  Every
+// CTA repeats it for its units; the weights' bytes still bound the unit, and a
+// launch and its 3 us are gone.  One token, k x n, one warp / four (us):
+// 4096 x 4096 10.4 / 9.6, 14336 x 4096 15.1 / 12.2, 8192 x 28672 34.3 / 26.6.
 template <typename T, int TN, int CG, bool FUSE>
-__global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
+__global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<TN, CG>::kThreads, 1)
     mx4_gemm_kernel(const MxParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
     using S = MxTile<TN, CG>;
     constexpr int ST = S::kStages;
+    constexpr int kThreads = FUSE ? S::kFuseThreads : S::kThreads;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     MxBars &bars = *reinterpret_cast<MxBars *>(smem);
@@ -778,7 +784,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
     }
     if (ahead) {
         __syncwarp();
-        asm volatile("barrier.cta.arrive 2, %0;\n" ::"n"(S::kThreads) : "memory");
+        asm volatile("barrier.cta.arrive 2, %0;\n" ::"n"(kThreads) : "memory");
     } else {
         if (warp == kMxMmaWarp)
             mx_tmem_alloc<CG>(&bars.tmem_slot);
@@ -817,7 +823,7 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             }
         }
         tc_fence_before();
-        asm volatile("barrier.cta.sync 2, %0;\n" ::"n"(S::kThreads) : "memory");
+        asm volatile("barrier.cta.sync 2, %0;\n" ::"n"(kThreads) : "memory");
         if constexpr (CG == 2)
             cluster_sync();  // the other CTA's barriers are ready
         tc_fence_after();
@@ -905,47 +911,54 @@ __global__ void __launch_bounds__(MxTile<TN, CG>::kThreads, 1)
             if (!ok && lane == 0)
                 record_timeout(p.status);
         }
-    } else if (FUSE && warp == kMxScaleWarp0 + 1) {
+    } else if (FUSE && (warp == kMxScaleWarp0 + 1 || warp >= S::kWarps)) {
         // ----------------------------------- quantising a token or two ---
         // Lane: block `lane & 3` of 32 columns of the unit's 128-column group
-        // (lane >> 2) & 3 of token lane >> 4.
+        // (lane >> 2) & 3 of token lane >> 4.  The worker's units go round the
+        // kMxQuantWarps warps: one alone took 0.95 us a unit, more than its
+        // weights' bytes do.
         const int l = lane & 3, grp = (lane >> 2) & 3, row = lane >> 4;
+        const int turn = warp >= S::kWarps ? warp - S::kWarps + 1 : 0;
         const bool mine = row < (int)p.rows;
         const T *const xr = (const T *)p.x + (int64_t)(mine ? row : 0) * p.k;
-        int s = 0;
+        int s = 0, who = 0;
         uint32_t round = 0;
         bool ok = true;
         for (int seg = 0; seg < sched.segs && ok; ++seg) {
             const MxSeg g = mx_seg(sched, seg);
-            for (int kb = g.k0; kb < g.k1 && ok; ++kb) {
-                const int col = kb * kMxBK + 128 * grp + 32 * l;
-                const bool there = col < p.k;  // with the rotation k ends with a group of 128
-                const int at = there ? col : 32 * l < p.k ? 32 * l : 0;
-                int byte = 0;
-                uint4 code;
-                if (p.rotate)
-                    code = quantize_block_rotated<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
-                else
-                    code = quantize_block<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
-                if (!there) {
-                    code = make_uint4(0u, 0u, 0u, 0u);
-                    byte = 0;
+            for (int kb = g.k0; kb < g.k1; ++kb) {
+                if (who == turn) {
+                    const int col = kb * kMxBK + 128 * grp + 32 * l;
+                    const bool there = col < p.k;  // with the rotation k ends with a group of 128
+                    const int at = there ? col : 32 * l < p.k ? 32 * l : 0;
+                    int byte = 0;
+                    uint4 code;
+                    if (p.rotate)
+                        code = quantize_block_rotated<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
+                    else
+                        code = quantize_block<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
+                    if (!there) {
+                        code = make_uint4(0u, 0u, 0u, 0u);
+                        byte = 0;
+                    }
+                    ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
+                    if (!ok)
+                        break;
+                    if (mine) {
+                        // row `row` of the box of columns 256 (grp / 2) on, 16-byte
+                        // chunk 4 (grp % 2) + l, at the place the swizzle gives it
+                        const int chunk = 4 * (grp & 1) + l;
+                        *reinterpret_cast<uint4 *>(bring + s * S::kBBytes + (grp >> 1) * (S::kBBytes / 2) + row * 128 +
+                                                   ((chunk ^ (row & 7)) << 4)) = code;
+                        scales[s * S::kScaleBytes + 2048 + 512 * grp + row * 16 + l] = (unsigned char)byte;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.full[s]);
                 }
-                ok = warp_wait_uniform(&bars.empty[s], (round & 1u) ^ 1u, p.wait_ns);
-                if (!ok)
-                    break;
-                if (mine) {
-                    // row `row` of the box of columns 256 (grp / 2) on, 16-byte
-                    // chunk 4 (grp % 2) + l, at the place the swizzle gives it
-                    const int chunk = 4 * (grp & 1) + l;
-                    *reinterpret_cast<uint4 *>(bring + s * S::kBBytes + (grp >> 1) * (S::kBBytes / 2) + row * 128 +
-                                               ((chunk ^ (row & 7)) << 4)) = code;
-                    scales[s * S::kScaleBytes + 2048 + 512 * grp + row * 16 + l] = (unsigned char)byte;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&bars.full[s]);
+                if (++who == kMxQuantWarps)
+                    who = 0;
                 if (++s == ST) {
                     s = 0;
                     ++round;
@@ -1275,7 +1288,7 @@ static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const C
         return EXL3_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(workers * CG));
-    cfg.blockDim = dim3(S::kThreads);
+    cfg.blockDim = dim3(FUSE ? S::kFuseThreads : S::kThreads);
     cfg.dynamicSmemBytes = (size_t)(S::kSmem + mx_table_bytes(p.experts));
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
