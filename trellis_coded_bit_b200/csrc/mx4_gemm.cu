@@ -48,7 +48,7 @@
 
 namespace exl3 {
 
-constexpr int kMxBM = 128;                       // output channels per CTA's tile (TMEM lanes)
+constexpr int kMxBM = 128;                       // output channels per CTA's tile, at most (TMEM lanes)
 constexpr int kMxBK = 512;                       // columns of k per unit: 16 scales of a row, two boxes of codes
 constexpr int kMxBoxK = 256;                     // columns of a box: 128 bytes of codes, the swizzle's width
 constexpr int kMxMmaWarp = 0, kMxTmaWarp = 1, kMxScaleWarp0 = 2, kMxEpiWarp0 = 4;
@@ -97,6 +97,7 @@ struct MxParams {
     uint32_t *status;
     int64_t rows;               // token rows
     int n, k, kb_count, experts, stride;
+    int bm;                     // output channels per CTA's tile: a multiple of 8; 128 with several experts or pairs
     uint32_t most;              // workers that share a split tile, at most
     uint64_t wait_ns;
     // FUSE: the activations themselves
@@ -300,7 +301,7 @@ __device__ __forceinline__ MxPlace mx_place(const MxParams &p, const MxTables &t
     MxPlace w;
     w.row = (int64_t)r0 + (int64_t)(local - nt * tts) * TN;
     w.row_end = r1;
-    w.ch = (int)nt * (kMxBM * CG);
+    w.ch = (int)nt * (p.bm * CG);
     w.wrow = (int64_t)lo * p.n + w.ch;
     return w;
 }
@@ -554,7 +555,8 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     const int64_t cols64 = w.row_end - w.row - c0;
     const int cols = cols64 < kCols ? (int)cols64 : kCols;         // this warp's tokens (may be <= 0)
     const int ch = w.ch + (int)rank * kMxBM + quarter * 32;        // the warp's first channel
-    const int ch_left = p.n - ch;
+    const int ch_end = w.ch + ((int)rank + 1) * p.bm;             // of this CTA's tile
+    const int ch_left = (ch_end < p.n ? ch_end : p.n) - ch;        // may be <= 0
     const bool wide = (p.n & 7) == 0;
     T *const y = reinterpret_cast<T *>(p.y) + (w.row + c0) * p.n + ch;
 
@@ -758,7 +760,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
     // copies waits for nobody: it sets up the barriers and begins the first stages
     // while the others set up.  What it reads before grid_dep_wait are weights
     // alone.
-    const uint32_t nts = (uint32_t)((p.n + kMxBM * CG - 1) / (kMxBM * CG));
+    const uint32_t nts = (uint32_t)((p.n + p.bm * CG - 1) / (p.bm * CG));
     const uint32_t tts = (uint32_t)((p.rows + TN - 1) / TN);  // without experts
     const bool early = CG == 1 && !p.offsets;
     const bool ahead = early && warp == kMxTmaWarp;
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                 col = (g.k0 + unit) * (kMxBK / 2);
                 row = (int)w.row;
-                mbar_arrive_expect_tx(&bars.full[lane], kMxABytes + (FUSE ? 0 : S::kBBytes));
+                mbar_arrive_expect_tx(&bars.full[lane], p.bm * (kMxBK / 2) + (FUSE ? 0 : S::kBBytes));
                 for (int h = 0; h < 2; ++h)
                     tma_load_2d<CG>(aring + lane * kMxABytes + h * (kMxABytes / 2), &wmap, col + h * (kMxBoxK / 2),
                                     (int)w.wrow, smem_addr(&bars.full[lane]));
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                     const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
                     if (elect_one()) {
                         if (rank == 0)
-                            mbar_arrive_expect_tx(&bars.full[s], CG * (kMxABytes + (FUSE ? 0 : S::kBBytes)));
+                            mbar_arrive_expect_tx(&bars.full[s], CG * (p.bm * (kMxBK / 2) + (FUSE ? 0 : S::kBBytes)));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
@@ -1080,7 +1082,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 fend = g.k1;
                 const int64_t tokens = w.row_end - w.row < TN ? w.row_end - w.row : TN;
                 const int ch = w.ch + (int)rank * kMxBM;
-                have = (half ? (int)tokens : p.n - ch) - lane;
+                const int channels = p.n - ch < p.bm ? p.n - ch : p.bm;
+                have = (half ? (int)tokens : channels) - lane;
                 from = half ? p.xs + (w.row + lane) * p.stride : p.ws + (w.wrow + (ch - w.ch) + lane) * p.stride;
                 if constexpr (NR > 4) {
                     have2 = (int)tokens - 128 - 64 * half - lane;
@@ -1266,6 +1269,35 @@ static uint32_t mx_most_workers(int tn, int kb)
     return w < 1.0 ? 1u : (uint32_t)w;
 }
 
+// Channels of a CTA's tile, and the workers that may share a tile.
+struct MxSplit {
+    int bm;
+    uint32_t most;
+};
+
+// Either tiles of 128 channels, some or all of them split along k, or, where one
+// token tile holds all rows and there is one expert, narrower tiles, as many as there are SMs (or once
+// or more again as many), each with all of k: nothing to add across CTAs, but a
+// unit of an eighth of the weights costs half of a whole one, 0.5 us against
+// 0.77, because its copies, scales and MMAs have their own minimum.  The sums of
+// split tiles cost 2 us and 0.03 us a token.  Split / narrow, us: 16 x 4096 x 4096
+// 8.7 / 8.7 (split), 32 x 4096 x 4096 10.4 / 9.2, 64 x 4096 x 4096 12.2 / 9.9, 64 x
+// 4096 x 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 / 31.1, 1 x 4096 x 14336 10.0 /
+// 9.4, 1 x 14336 x 4096 11.4 / 17.4 (split).
+static MxSplit mx_split(int64_t rows, int64_t n, int kb, int64_t experts, int tn)
+{
+    const MxSplit shared = {kMxBM, mx_most_workers(tn, kb)};
+    if (experts > 1 || tn > 128 || rows > tn || kb == 1)
+        return shared;
+    const int64_t sms = num_sms(), tiles = (n + kMxBM - 1) / kMxBM;
+    const int64_t rounds = (tiles + sms - 1) / sms;
+    const int bm = (int)((n + sms * rounds - 1) / (sms * rounds) + 7) / 8 * 8;  // at most 128
+    const double unit = 0.006 * bm > 0.5 ? 0.006 * bm : 0.5;
+    const double narrow = unit * (double)(rounds * kb);
+    const double split = 0.77 * (double)(tiles * kb) / (double)sms + 2.0 + 0.03 * tn;
+    return narrow < split ? MxSplit{bm, 1u} : shared;
+}
+
 static size_t mx_workspace(int64_t rows, int64_t n, int64_t experts)
 {
     return kMxSyncArea + (size_t)2 * num_sms() * mx_token_tile(rows, n, experts) * kMxBM * 4;
@@ -1353,9 +1385,12 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
 {
     const int tn = mx_token_tile(m, n, experts);
     const int cg = tn > 128 ? 2 : 1;  // CTAs that share a tile
+    const int64_t kb_count = (k + kMxBK - 1) / kMxBK;
+    const MxSplit split = mx_split(m, n, (int)kb_count, experts, tn);
+    const int bm = split.bm;
     CUtensorMap wmap, xmap;
     // (with x the tokens' map is not used)
-    if (!code_map(&wmap, wc, experts * n, k / 2, kMxBM) || !code_map(&xmap, x ? wc : xc, x ? n : m, k / 2, tn / cg))
+    if (!code_map(&wmap, wc, experts * n, k / 2, bm) || !code_map(&xmap, x ? wc : xc, x ? n : m, k / 2, tn / cg))
         return EXL3_ERR_CUDA;
     MxParams p;
     p.x = x;
@@ -1371,14 +1406,15 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     p.rows = m;
     p.n = (int)n;
     p.k = (int)k;
-    p.kb_count = (int)((k + kMxBK - 1) / kMxBK);
+    p.kb_count = (int)kb_count;
+    p.bm = bm;
     p.experts = (int)experts;
     p.stride = (int)mx4_scale_stride(k);
-    p.most = mx_most_workers(tn, p.kb_count);
+    p.most = split.most;
     p.wait_ns = wait_limit_ns();
     // units fit 32 bits: at most (rows/TN + experts) tiles of each channel row
     const int64_t tiles =
-        ((m + tn - 1) / tn + (experts > 1 ? experts : 0)) * ((n + kMxBM * cg - 1) / (kMxBM * cg));
+        ((m + tn - 1) / tn + (experts > 1 ? experts : 0)) * ((n + bm * cg - 1) / (bm * cg));
     if (tiles * p.kb_count >= (int64_t)1 << 31)
         return EXL3_ERR_UNSUPPORTED;
     const int64_t most = num_sms() / cg;
