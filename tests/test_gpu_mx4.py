@@ -210,7 +210,9 @@ SHAPES = [(1, 32, 1), (1, 256, 128), (1, 64, 5), (2, 96, 129), (16, 128, 128), (
           # a long sum
           (3, 262144, 40),
           # tiles of fewer channels than 128, one or two for each SM, odd and cut ones
-          (40, 4096, 4100), (100, 1536, 19001), (128, 640, 333), (20, 1056, 30011), (1, 4096, 14344), (64, 8192, 1000)]
+          (40, 4096, 4100), (100, 1536, 19001), (128, 640, 333), (20, 1056, 30011), (1, 4096, 14344), (64, 8192, 1000),
+          # the same with several token tiles
+          (129, 8192, 2056), (333, 4000, 5001), (1000, 1056, 700)]
 
 
 @pytest.mark.parametrize("m,k,n", SHAPES)

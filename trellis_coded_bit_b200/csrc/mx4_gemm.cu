@@ -1275,27 +1275,27 @@ struct MxSplit {
     uint32_t most;
 };
 
-// Either tiles of 128 channels, some or all of them split along k, or, where one
-// token tile holds all rows and there is one expert, narrower tiles, as many as there are SMs (or once
-// or more again as many), each with all of k: nothing to add across CTAs, but a
-// unit of an eighth of the weights costs half of a whole one, 0.5 us against
-// 0.77, because its copies, scales and MMAs have their own minimum.  The sums of
-// split tiles cost 2 us and 0.03 us a token.  Split / narrow, us: 16 x 4096 x 4096
-// 8.7 / 8.7 (split), 32 x 4096 x 4096 10.4 / 9.2, 64 x 4096 x 4096 12.2 / 9.9, 64 x
-// 4096 x 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 / 31.1, 1 x 4096 x 14336 10.0 /
-// 9.4, 1 x 14336 x 4096 11.4 / 17.4 (split).
+// Either tiles of 128 channels, some or all of them split along k, or, on single
+// CTAs and with one expert, narrower tiles, as many as there are SMs (or that
+// many times 2, 3, ..), each with all of k: nothing to add across CTAs, but a unit
+// of an eighth of the weights costs half of a whole one, 0.5 us against 0.77,
+// because its copies, scales and MMAs have their own minimum.  The sums of split
+// tiles cost 2 us and 0.03 us a token.  Split / narrow, us: 16 x 4096 x 4096 8.7 /
+// 8.7 (split), 32 x 4096 x 4096 10.4 / 9.2, 64 x 4096 x 4096 12.2 / 9.9, 64 x 4096 x
+// 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 / 31.1, 129 x 8192 x 8192 22.5 / 15.1,
+// 1 x 4096 x 14336 10.0 / 9.4, 1 x 14336 x 4096 11.4 / 17.4 (split).
 static MxSplit mx_split(int64_t rows, int64_t n, int kb, int64_t experts, int tn)
 {
     const MxSplit shared = {kMxBM, mx_most_workers(tn, kb)};
-    if (experts > 1 || tn > 128 || rows > tn || kb == 1)
+    if (experts > 1 || tn > 128 || kb == 1)
         return shared;
-    const int64_t sms = num_sms(), tiles = (n + kMxBM - 1) / kMxBM;
-    const int64_t rounds = (tiles + sms - 1) / sms;
-    const int bm = (int)((n + sms * rounds - 1) / (sms * rounds) + 7) / 8 * 8;  // at most 128
+    const int64_t sms = num_sms(), tts = (rows + tn - 1) / tn, nts = (n + kMxBM - 1) / kMxBM;
+    const int64_t rounds = (tts * nts + sms - 1) / sms, most = sms * rounds / tts;  // most >= nts
+    const int bm = (int)((n + most - 1) / most + 7) / 8 * 8;                         // at most 128
     const double unit = 0.006 * bm > 0.5 ? 0.006 * bm : 0.5;
     const double narrow = unit * (double)(rounds * kb);
-    const double split = 0.77 * (double)(tiles * kb) / (double)sms + 2.0 + 0.03 * tn;
-    return narrow < split ? MxSplit{bm, 1u} : shared;
+    const double split = 0.77 * (double)(tts * nts * kb) / (double)sms + 2.0 + 0.03 * tn;
+    return shared.most == 1 || narrow < split ? MxSplit{bm, 1u} : shared;
 }
 
 static size_t mx_workspace(int64_t rows, int64_t n, int64_t experts)
