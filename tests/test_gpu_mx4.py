@@ -212,7 +212,10 @@ SHAPES = [(1, 32, 1), (1, 256, 128), (1, 64, 5), (2, 96, 129), (16, 128, 128), (
           # tiles of fewer channels than 128, one or two for each SM, odd and cut ones
           (40, 4096, 4100), (100, 1536, 19001), (128, 640, 333), (20, 1056, 30011), (1, 4096, 14344), (64, 8192, 1000),
           # the same with several token tiles
-          (129, 8192, 2056), (333, 4000, 5001), (1000, 1056, 700)]
+          (129, 8192, 2056), (333, 4000, 5001), (1000, 1056, 700),
+          # two or four parts of k side by side: whole, cut and missing ones, odd channels
+          (1, 2048, 4096), (2, 2080, 1001), (3, 1056, 5000), (4, 4000, 4737), (5, 1088, 300), (8, 5632, 8192),
+          (7, 2592, 2049), (4, 1184, 3), (1, 14336, 4000), (1, 8192, 9480)]
 
 
 @pytest.mark.parametrize("m,k,n", SHAPES)
@@ -308,7 +311,7 @@ def test_product_large_and_repeatable():
 @pytest.mark.parametrize("dtype", TYPES[:2])
 @pytest.mark.parametrize("m,k,n,rotate", [(1, 4096, 512, True), (5, 256, 130, True), (70, 1024, 200, False),
                                           (1, 96, 33, False), (300, 512, 256, True), (2, 128, 40, True), (2, 1152, 4200, True),
-                                          (2, 32, 300, False), (1, 1056, 129, False), (1, 14336, 640, True), (3, 640, 128, True)])
+                                          (2, 32, 300, False), (1, 1056, 129, False), (1, 2080, 4097, False), (2, 4096, 4096, True), (1, 8192, 5000, True), (1, 14336, 640, True), (3, 640, 128, True)])
 def test_linear_is_quantize_then_product(dtype, m, k, n, rotate):
     rng = np.random.default_rng(m + n)
     x = torch.from_numpy(rng.standard_normal((m, k))).to(dtype).cuda()
@@ -351,6 +354,31 @@ def test_linear_of_infinities_and_values_beside_borders(m):
 
 
 # ----------------------------------------------------------------- experts ---
+
+@pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("m,k,n", [(1, 512, 300), (2, 512, 300), (1, 2048, 2048), (2, 4096, 520)])
+def test_linear_of_codes_beside_ties(dtype, m, k, n):
+    """Rotated values within 2^-24 of the tie between the codes 4 and 6, on both
+    sides, whole blocks of them, some in every unit: the layer's own
+    quantisation takes the codes of the exact sums."""
+    rng = np.random.default_rng(k + m)
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(dtype)
+    for row in range(m):
+        for g in range(row, k // 128, 3):
+            left = 5.0 * np.sqrt(128.0) + (g % 2 * 2 - 1) * 2.0 ** -21  # the tie, scaled by sqrt(128)
+            x[row, 128 * g:128 * (g + 1)] = 0
+            for col in (0, 32, 64, 96):   # one Walsh row is their sum; the others differ by signs
+                part = torch.tensor(left, dtype=torch.float64).to(dtype)
+                x[row, 128 * g + col] = part
+                left -= float(part)
+            assert abs(left) < 2.0 ** -20
+    wc, wsc = exl3.exl3_mx4_quantize(torch.from_numpy(rng.standard_normal((n, k))).float().cuda())
+    ws = exl3.new_workspace(exl3.exl3_mx4_linear_workspace_size(m, k, n))
+    y = exl3.exl3_mx4_linear(x.cuda(), wc, wsc, rotate=True, workspace=ws)
+    codes, scales = mx4.quantize(mx4.rotate(host(x), None))
+    xc, xs = (dev(v) for v in mx4.pack(codes, scales))
+    assert torch.equal(y, exl3.exl3_mx4_matmul(xc, xs, wc, wsc, dtype=dtype, workspace=ws))
+
 
 def experts_case(rng, counts, k, n, spare=0, low=120, high=127):
     counts = np.asarray(counts)

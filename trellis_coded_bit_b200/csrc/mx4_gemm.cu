@@ -18,7 +18,9 @@
 // codes, and the pair's MMAs read both), which moves a third fewer bytes per
 // product.  mx_schedule says how tiles are shared out; where several workers share
 // one, each writes its fp32 partial sums and the last to arrive (atomic ticket, no
-// spinning) adds them in a fixed order, so results are deterministic.
+// spinning) adds them in a fixed order, so results are deterministic.  Small
+// products take tiles of fewer channels instead, each with all of k, and for a few
+// tokens with parts of k side by side in one MMA (mx_split).
 //
 // Warps: 0 MMA issuer, 1 copies (TMA, 128-byte swizzled boxes of 256 columns), 2
 // and 3 scales, 4 .. epilogue.  Scales are row-major in memory; the tensor core
@@ -27,9 +29,9 @@
 // them out to the stages in that order, and tcgen05.cp broadcasts a stage's to the
 // TMEM columns that belong to the stage.
 //
-// What bounds it: few tokens, the weights' bytes (32 x 8192 x 28672: 28 us, 4.5
+// What bounds it: few tokens, the weights' bytes (32 x 8192 x 28672: 27 us, 4.6
 // TB/s, of which 19 us are the bytes and most of the rest the first copy's 2.6 us,
-// the start, and the sums of split tiles); many, the supply of the tensor cores at
+// the start, and uneven SMs); many, the supply of the tensor cores at
 // the ends of tiles (2048 x 8192 x 28672: 201 us, 4.8 PFLOP/s; within a tile a unit
 // takes 1050 cycles, the MMAs' own time, and while the tile before is stored
 // 2000).
@@ -56,6 +58,7 @@ constexpr int kMxABytes = kMxBM * kMxBK / 2;     // 32 KB
 constexpr int kMxMaxExperts = 512;
 constexpr int kMxFuseRows = 2;                   // tokens that the product of a layer quantises itself
 constexpr int kMxQuantWarps = 4;                 // warps that quantise them
+constexpr int kMxFoldRows = 4;                   // tokens of a product whose tiles hold parts of k side by side
 constexpr size_t kMxSyncArea = 64 * 1024;
 // Shared memory of the experts' tables: each one's first tile and first row.
 constexpr int mx_table_bytes(int experts)
@@ -96,8 +99,10 @@ struct MxParams {
     uint32_t *counters;         // [split tiles, fewer than workers][CG]
     uint32_t *status;
     int64_t rows;               // token rows
-    int n, k, kb_count, experts, stride;
+    int n, k, experts, stride;
+    int kb_count;               // units: of 512 columns of each part
     int bm;                     // output channels per CTA's tile: a multiple of 8; 128 with several experts or pairs
+    int fold;                   // log2 of the parts of k side by side in a tile (FOLD, kMxFoldRows tokens at most; else 0)
     uint32_t most;              // workers that share a split tile, at most
     uint64_t wait_ns;
     // FUSE: the activations themselves
@@ -511,7 +516,7 @@ __device__ __forceinline__ void mx_release(MxBars &bars, int acc)
 
 // Segment `seg` of this worker.  Returns false if its accumulators never came
 // (the caller stops).
-template <typename T, int TN, int CG>
+template <typename T, int TN, int CG, bool FOLD>
 __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, const MxTables &tab, const MxSched &sched,
                                             uint32_t tmem, int seg, uint32_t rank)
 {
@@ -559,6 +564,34 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
     const int ch_left = (ch_end < p.n ? ch_end : p.n) - ch;        // may be <= 0
     const bool wide = (p.n & 7) == 0;
     T *const y = reinterpret_cast<T *>(p.y) + (w.row + c0) * p.n + ch;
+
+    if constexpr (FOLD) {
+        // Each part's sums lie in its own lanes and columns; they meet in
+        // shared memory, added in the order of k.  (The tile is whole, and the
+        // barriers above keep the sums of the tile before until they are read.)
+        __shared__ float sums[4][kMxFoldRows][32];
+        const int warps = 4 >> p.fold;                // warps of a part
+        const int part = quarter >> (2 - p.fold);
+        uint32_t b[16];
+        EXL3_TMEM_LD16(d + part * (16 >> p.fold), b);  // (behind the tokens' columns: not used)
+        mx_release<CG>(bars, acc);
+#pragma unroll
+        for (int i = 0; i < kMxFoldRows; ++i)
+            sums[quarter][i][lane] = __uint_as_float(b[i]);
+        mx_epi_sync<TN, CG>();
+        if (part == 0 && lane < ch_left) {
+#pragma unroll
+            for (int i = 0; i < kMxFoldRows; ++i) {
+                if (i < cols) {
+                    float s = sums[quarter][i][lane];
+                    for (int j = 1; j < 1 << p.fold; ++j)
+                        s += sums[quarter + j * warps][i][lane];
+                    y[(int64_t)i * p.n + lane] = from_f32<T>(s);
+                }
+            }
+        }
+        return true;
+    }
 
     if constexpr (sizeof(T) == 4) {
         // fp32: a warp's 32 channels of a token are 128 contiguous bytes as
@@ -732,11 +765,12 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
 // FUSE: the tokens (kMxFuseRows at most) come as rows of T, and kMxQuantWarps
 // warps in turn (one of them in the place of the warp that would deal out the
 // tokens' scales) quantise them, codes and scales, straight into the stage: 4
-// lanes a rotation, 16 a token and unit, so one pass of a warp a unit.  Every
-// CTA repeats it for its units; the weights' bytes still bound the unit, and a
-// launch and its 3 us are gone.  One token, k x n, one warp / four (us):
-// 4096 x 4096 10.4 / 9.6, 14336 x 4096 15.1 / 12.2, 8192 x 28672 34.3 / 26.6.
-template <typename T, int TN, int CG, bool FUSE>
+// lanes a rotation, 16 a token and unit, so one pass of a warp a unit (and part of
+// k).  Every CTA repeats it for its units, and a launch and its 3 us are gone.  One
+// token, k x n, one warp / four (us): 4096 x 4096 10.4 / 9.6, 14336 x 4096 15.1 /
+// 12.2, 8192 x 28672 34.3 / 26.6.
+// FOLD: 2^p.fold parts of k side by side (mx_split).
+template <typename T, int TN, int CG, bool FUSE, bool FOLD>
 __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<TN, CG>::kThreads, 1)
     mx4_gemm_kernel(const MxParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
@@ -754,6 +788,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
     const MxTables tab{first, frow, p.experts};
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int fold = FOLD ? p.fold : 0;
     const uint32_t rank = CG == 1 ? 0u : cluster_rank();
     const uint32_t worker = blockIdx.x / CG;
     // Without experts the tiles are known at once, and the warp that issues the
@@ -766,7 +801,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
     const bool ahead = early && warp == kMxTmaWarp;
     if (threadIdx.x == 32 * kMxTmaWarp) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&bars.full[s], 1 + CG * 2);  // the bytes, each CTA's scale warps
+            // the bytes, each CTA's scale warps; or the weights' and each part of the tokens
+            mbar_init(&bars.full[s], FUSE ? 2 + (1 << fold) : 1 + CG * 2);
             mbar_init(&bars.empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -861,7 +897,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                     const uint64_t adesc = smem_desc(a_base + (uint32_t)(s * kMxABytes), 16, 1024);
                     const uint64_t bdesc = smem_desc(b_base + (uint32_t)(s * S::kBBytes), 16, 1024);
                     const int left = p.k - kb * kMxBK;
-                    const int steps = left >= kMxBK ? 8 : (left + 63) / 64;  // 64 columns per MMA; none behind k
+                    // 64 columns per MMA; none behind k, where all parts end there
+                    const int steps = left >= kMxBK || fold ? 8 : (left + 63) / 64;
                     uint64_t *const done = &bars.empty[s];
                     if (elect_one()) {
                         // chunk c's scales: weights at tsa + 4c, tokens at tsb + 4 groups c
@@ -916,8 +953,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
     } else if (FUSE && (warp == kMxScaleWarp0 + 1 || warp >= S::kWarps)) {
         // ----------------------------------- quantising a token or two ---
         // Lane: block `lane & 3` of 32 columns of the unit's 128-column group
-        // (lane >> 2) & 3 of token lane >> 4.  The worker's units go round the
-        // kMxQuantWarps warps: one alone took 0.95 us a unit, more than its
+        // (lane >> 2) & 3 of token lane >> 4.  The worker's units (of each part of
+        // k) go round the kMxQuantWarps warps: one alone took 0.95 us a unit, more than its
         // weights' bytes do.
         const int l = lane & 3, grp = (lane >> 2) & 3, row = lane >> 4;
         const int turn = warp >= S::kWarps ? warp - S::kWarps + 1 : 0;
@@ -928,15 +965,20 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
         bool ok = true;
         for (int seg = 0; seg < sched.segs && ok; ++seg) {
             const MxSeg g = mx_seg(sched, seg);
-            for (int kb = g.k0; kb < g.k1; ++kb) {
-                if (who == turn) {
-                    const int col = kb * kMxBK + 128 * grp + 32 * l;
+            for (int kb = g.k0; kb < g.k1 && ok; ++kb) {
+                for (int j = 0; j < 1 << fold; ++j) {
+                    const bool my_turn = who == turn;
+                    if (++who == kMxQuantWarps)
+                        who = 0;
+                    if (!my_turn)
+                        continue;
+                    const int col = (kb + j * KB) * kMxBK + 128 * grp + 32 * l;
                     const bool there = col < p.k;  // with the rotation k ends with a group of 128
                     const int at = there ? col : 32 * l < p.k ? 32 * l : 0;
                     int byte = 0;
                     uint4 code;
                     if (p.rotate)
-                        code = quantize_block_rotated<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
+                        code = quantize_block_rotated<T, true>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
                     else
                         code = quantize_block<T>(xr + at, p.signs ? p.signs + at : nullptr, &byte);
                     if (!there) {
@@ -947,20 +989,18 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                     if (!ok)
                         break;
                     if (mine) {
-                        // row `row` of the box of columns 256 (grp / 2) on, 16-byte
+                        // row `at_row` of the box of columns 256 (grp / 2) on, 16-byte
                         // chunk 4 (grp % 2) + l, at the place the swizzle gives it
-                        const int chunk = 4 * (grp & 1) + l;
-                        *reinterpret_cast<uint4 *>(bring + s * S::kBBytes + (grp >> 1) * (S::kBBytes / 2) + row * 128 +
-                                                   ((chunk ^ (row & 7)) << 4)) = code;
-                        scales[s * S::kScaleBytes + 2048 + 512 * grp + row * 16 + l] = (unsigned char)byte;
+                        const int chunk = 4 * (grp & 1) + l, at_row = j * (TN >> fold) + row;
+                        *reinterpret_cast<uint4 *>(bring + s * S::kBBytes + (grp >> 1) * (S::kBBytes / 2) + at_row * 128 +
+                                                   ((chunk ^ (at_row & 7)) << 4)) = code;
+                        scales[s * S::kScaleBytes + 2048 + 512 * grp + at_row * 16 + l] = (unsigned char)byte;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bars.full[s]);
                 }
-                if (++who == kMxQuantWarps)
-                    who = 0;
                 if (++s == ST) {
                     s = 0;
                     ++round;
@@ -992,18 +1032,21 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 const MxPlace w = mx_place<TN, CG>(p, tab, g.t);
                 col = (g.k0 + unit) * (kMxBK / 2);
                 row = (int)w.row;
-                mbar_arrive_expect_tx(&bars.full[lane], p.bm * (kMxBK / 2) + (FUSE ? 0 : S::kBBytes));
+                mbar_arrive_expect_tx(&bars.full[lane], ((p.bm * (kMxBK / 2)) << fold) + (FUSE ? 0 : S::kBBytes));
                 for (int h = 0; h < 2; ++h)
-                    tma_load_2d<CG>(aring + lane * kMxABytes + h * (kMxABytes / 2), &wmap, col + h * (kMxBoxK / 2),
-                                    (int)w.wrow, smem_addr(&bars.full[lane]));
+                    for (int j = 0; j < 1 << fold; ++j)
+                        tma_load_2d<CG>(aring + lane * kMxABytes + h * (kMxABytes / 2) + j * (kMxABytes / 2 >> fold), &wmap,
+                                        col + h * (kMxBoxK / 2) + j * KB * (kMxBK / 2), (int)w.wrow,
+                                        smem_addr(&bars.full[lane]));
             }
             pre = __popc(__ballot_sync(0xffffffffu, mine));
             grid_dep_wait();
             grid_dep_launch();
             if (mine && !FUSE)
                 for (int h = 0; h < 2; ++h)
-                    tma_load_2d<CG>(bring + lane * S::kBBytes + h * (S::kBBytes / 2), &xmap, col + h * (kMxBoxK / 2), row,
-                                    smem_addr(&bars.full[lane]));
+                    for (int j = 0; j < 1 << fold; ++j)
+                        tma_load_2d<CG>(bring + lane * S::kBBytes + h * (S::kBBytes / 2) + j * (S::kBBytes / 2 >> fold), &xmap,
+                                        col + h * (kMxBoxK / 2) + j * KB * (kMxBK / 2), row, smem_addr(&bars.full[lane]));
         }
         uint32_t round = 0;                  // of the ring
         uint32_t issued = (1u << pre) - 1u;  // stages that were ever filled: bits
@@ -1022,13 +1065,18 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                     const uint32_t bar = CG == 1 ? smem_addr(&bars.full[s]) : leader_addr(&bars.full[s]);
                     if (elect_one()) {
                         if (rank == 0)
-                            mbar_arrive_expect_tx(&bars.full[s], CG * (p.bm * (kMxBK / 2) + (FUSE ? 0 : S::kBBytes)));
+                            mbar_arrive_expect_tx(&bars.full[s],
+                                                  CG * (((p.bm * (kMxBK / 2)) << fold) + (FUSE ? 0 : S::kBBytes)));
+                        for (int j = 0; j < 1 << fold; ++j) {
+                            unsigned char *const a = aring + s * kMxABytes + j * (kMxABytes / 2 >> fold);
+                            unsigned char *const b = bring + s * S::kBBytes + j * (S::kBBytes / 2 >> fold);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int col = kb * (kMxBK / 2) + h * (kMxBoxK / 2);
-                            tma_load_2d<CG>(aring + s * kMxABytes + h * (kMxABytes / 2), &wmap, col, wrow, bar);
-                            if constexpr (!FUSE)
-                                tma_load_2d<CG>(bring + s * S::kBBytes + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
+                            for (int h = 0; h < 2; ++h) {
+                                const int col = (kb + j * KB) * (kMxBK / 2) + h * (kMxBoxK / 2);
+                                tma_load_2d<CG>(a + h * (kMxABytes / 2), &wmap, col, wrow, bar);
+                                if constexpr (!FUSE)
+                                    tma_load_2d<CG>(b + h * (S::kBBytes / 2), &xmap, col, xrow, bar);
+                            }
                         }
                     }
                     __syncwarp();
@@ -1074,6 +1122,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
         int fseg = 0, fkb = 0, fend = 0;
         const uint8_t *from = nullptr, *from2 = nullptr;  // scales of rows `lane` and 128 + 64 half + lane
         int have = 0, have2 = 0;                          // rows from there on that exist
+        // the part of k of row lane + 32 j
+        auto part_of = [&](int j) { return half ? (lane & 15) >> (4 - fold) : j >> (2 - fold); };
         auto enter = [&]() {
             if (fseg < sched.segs) {
                 const MxSeg g = mx_seg(sched, fseg);
@@ -1083,8 +1133,10 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 const int64_t tokens = w.row_end - w.row < TN ? w.row_end - w.row : TN;
                 const int ch = w.ch + (int)rank * kMxBM;
                 const int channels = p.n - ch < p.bm ? p.n - ch : p.bm;
-                have = (half ? (int)tokens : channels) - lane;
-                from = half ? p.xs + (w.row + lane) * p.stride : p.ws + (w.wrow + (ch - w.ch) + lane) * p.stride;
+                // (row of a token: lane, in a part's rows)
+                const int mine = half && FOLD ? lane & ((16 >> fold) - 1) : lane;
+                have = half && FOLD && lane >= 16 ? 0 : (half ? (int)tokens : channels) - mine;
+                from = half ? p.xs + (w.row + mine) * p.stride : p.ws + (w.wrow + (ch - w.ch) + lane) * p.stride;
                 if constexpr (NR > 4) {
                     have2 = (int)tokens - 128 - 64 * half - lane;
                     from2 = p.xs + (w.row + 128 + 64 * half + lane) * p.stride;
@@ -1096,9 +1148,19 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
             if (fseg >= sched.segs)
                 return;
             const int64_t col = (int64_t)fkb * 16, hop = (int64_t)32 * p.stride;
+            if constexpr (FOLD) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                q[j] = 32 * j < have ? *reinterpret_cast<const uint4 *>(from + col + j * hop) : make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < 4; ++j) {
+                    const int part = part_of(j), rows = half ? 32 * j : 32 * (j & ((4 >> fold) - 1));
+                    q[j] = rows < have && 16 * (fkb + part * KB) < p.stride
+                               ? *reinterpret_cast<const uint4 *>(from + col + (int64_t)part * KB * 16 + (int64_t)rows * p.stride)
+                               : make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = 32 * j < have ? *reinterpret_cast<const uint4 *>(from + col + j * hop) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
             for (int j = 4; j < NR; ++j)
                 q[j] = 32 * (j - 4) < have2 ? *reinterpret_cast<const uint4 *>(from2 + col + (j - 4) * hop)
@@ -1132,7 +1194,8 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                         unsigned char *sc = scales + s * S::kScaleBytes + lane * 16;
                         unsigned char *main = sc + (half ? 2048 : 0);
                         const int step = half ? 512 * S::kBGroups : 512;
-                        const int left = kblocks - kb * (kMxBK / kMx4Block);  // scales that exist from this unit on
+                        const int last = FOLD ? kb + ((1 << fold) - 1) * KB : kb;
+                        const int left = kblocks - last * (kMxBK / kMx4Block);  // scales that exist from this unit on
                         uint32_t v[4][NR];                                    // [128 columns][row]
 #pragma unroll
                         for (int j = 0; j < NR; ++j) {
@@ -1144,11 +1207,12 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                         if (left < kMxBK / kMx4Block) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                const int n4 = left - 4 * c;
-                                const uint32_t keep = n4 >= 4 ? 0xffffffffu : (n4 <= 0 ? 0u : (1u << (8 * n4)) - 1u);
 #pragma unroll
-                                for (int j = 0; j < NR; ++j)
-                                    v[c][j] &= keep;
+                                for (int j = 0; j < NR; ++j) {
+                                    const int at = FOLD ? kb + part_of(j) * KB : kb;
+                                    const int n4 = kblocks - at * (kMxBK / kMx4Block) - 4 * c;
+                                    v[c][j] &= n4 >= 4 ? 0xffffffffu : (n4 <= 0 ? 0u : (1u << (8 * n4)) - 1u);
+                                }
                             }
                         }
 #pragma unroll
@@ -1188,7 +1252,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
     } else {
         // ---------------------------------------------------- epilogue ---
         for (int seg = 0; seg < sched.segs; ++seg)
-            if (!mx_epilogue<T, TN, CG>(p, bars, tab, sched, bars.tmem_slot, seg, rank))
+            if (!mx_epilogue<T, TN, CG, FOLD>(p, bars, tab, sched, bars.tmem_slot, seg, rank))
                 break;
     }
 
@@ -1269,33 +1333,55 @@ static uint32_t mx_most_workers(int tn, int kb)
     return w < 1.0 ? 1u : (uint32_t)w;
 }
 
-// Channels of a CTA's tile, and the workers that may share a tile.
+// Channels of a CTA's tile, log2 of the parts of k in it, and the workers that may
+// share a tile.
 struct MxSplit {
     int bm;
+    int fold;
     uint32_t most;
 };
 
-// Either tiles of 128 channels, some or all of them split along k, or, on single
-// CTAs and with one expert, narrower tiles, as many as there are SMs (or that
-// many times 2, 3, ..), each with all of k: nothing to add across CTAs, but a unit
-// of an eighth of the weights costs half of a whole one, 0.5 us against 0.77,
-// because its copies, scales and MMAs have their own minimum.  The sums of split
-// tiles cost 2 us and 0.03 us a token.  Split / narrow, us: 16 x 4096 x 4096 8.7 /
-// 8.7 (split), 32 x 4096 x 4096 10.4 / 9.2, 64 x 4096 x 4096 12.2 / 9.9, 64 x 4096 x
-// 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 / 31.1, 129 x 8192 x 8192 22.5 / 15.1,
-// 1 x 4096 x 14336 10.0 / 9.4, 1 x 14336 x 4096 11.4 / 17.4 (split).
+// Three ways, by the time that each should take (us, without what all have):
+// - tiles of 128 channels, some or all split along k over several CTAs: a unit's
+//   bytes take 0.77, the sums of split tiles 2 and 0.03 a token;
+// - on single CTAs and with one expert, narrower tiles, as many as there are SMs
+//   (or that many times 2, 3, ..), each with all of k: nothing to add across CTAs,
+//   but a unit of an eighth of the weights still takes 0.5, for its copies,
+//   scales and MMAs;
+// - for kMxFoldRows tokens, 2 or 4 such narrow tiles' parts of k side by side in
+//   one MMA: the channels repeat in the lanes and the tokens in the columns, the
+//   sums of part j are where its lanes meet its columns (the rest is not used),
+//   and a tile has a half or a quarter of the units.
+// Where the product quantises the tokens itself, each CTA does so for its columns
+// of k, 0.25 for 512.  (A product of as many rows takes the same way, so that both
+// sum in the same order.)
+// First / second, us: 16 x 4096 x 4096 8.7 / 8.7 (first), 32 x 4096 x 4096 10.4 / 9.2,
+// 64 x 4096 x 4096 12.2 / 9.9, 64 x 4096 x 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 /
+// 31.1, 129 x 8192 x 8192 22.5 / 15.1, 1 x 4096 x 14336 10.0 / 9.4, 1 x 14336 x 4096
+// 11.4 / 17.4 (first).  First / third: 1 x 2048 x 2048 6.9 / 5.6, 1 x 4096 x 4096 8.5 /
+// 7.4, 1 x 8192 x 8192 11.9 / 10.3; quantising too 8.4 / 6.7, 9.8 / 9.1, 13.3 / 13.3, and 1 x
+// 14336 x 4096 12.6 / 16.8 (first).
 static MxSplit mx_split(int64_t rows, int64_t n, int kb, int64_t experts, int tn)
 {
-    const MxSplit shared = {kMxBM, mx_most_workers(tn, kb)};
+    MxSplit best = {kMxBM, 0, mx_most_workers(tn, kb)};
     if (experts > 1 || tn > 128 || kb == 1)
-        return shared;
-    const int64_t sms = num_sms(), tts = (rows + tn - 1) / tn, nts = (n + kMxBM - 1) / kMxBM;
-    const int64_t rounds = (tts * nts + sms - 1) / sms, most = sms * rounds / tts;  // most >= nts
-    const int bm = (int)((n + most - 1) / most + 7) / 8 * 8;                         // at most 128
-    const double unit = 0.006 * bm > 0.5 ? 0.006 * bm : 0.5;
-    const double narrow = unit * (double)(rounds * kb);
-    const double split = 0.77 * (double)(tts * nts * kb) / (double)sms + 2.0 + 0.03 * tn;
-    return shared.most == 1 || narrow < split ? MxSplit{bm, 1u} : shared;
+        return best;
+    const int64_t sms = num_sms(), tts = (rows + tn - 1) / tn;
+    const double units = (double)(tts * ((n + kMxBM - 1) / kMxBM) * kb) / (double)sms;
+    const double quantise = rows <= kMxFuseRows ? 0.25 : 0.0;
+    double time = best.most == 1 ? 1e30 : (0.77 + quantise) * units + 2.0 + 0.03 * tn;
+    for (int fold = 0; fold <= 2 && 1 << fold <= kb && (fold == 0 || rows <= kMxFoldRows); ++fold) {
+        const int64_t nts = (n + (kMxBM >> fold) - 1) / (kMxBM >> fold);
+        const int64_t rounds = (tts * nts + sms - 1) / sms, most = sms * rounds / tts;  // most >= nts
+        const int bm = (int)((n + most - 1) / most + 7) / 8 * 8;                         // at most 128 >> fold
+        const double unit = 0.006 * (bm << fold) > 0.5 ? 0.006 * (bm << fold) : 0.5;
+        const double narrow = unit * (double)(rounds * ((kb + (1 << fold) - 1) >> fold)) + quantise * (double)(rounds * kb);
+        if (narrow < time) {
+            time = narrow;
+            best = MxSplit{bm, fold, 1u};
+        }
+    }
+    return best;
 }
 
 static size_t mx_workspace(int64_t rows, int64_t n, int64_t experts)
@@ -1309,12 +1395,12 @@ static bool valid_mx_sizes(int64_t m, int64_t k, int64_t n, int64_t experts)
            experts <= kMxMaxExperts && experts * n <= (int64_t)1 << 30;
 }
 
-template <typename T, int TN, int CG, bool FUSE = false>
+template <typename T, int TN, int CG, bool FUSE = false, bool FOLD = false>
 static exl3_status launch_mx(const MxParams &p, const CUtensorMap &wmap, const CUtensorMap &xmap, int workers, bool pdl,
                              cudaStream_t s)
 {
     using S = MxTile<TN, CG>;
-    auto kern = mx4_gemm_kernel<T, TN, CG, FUSE>;
+    auto kern = mx4_gemm_kernel<T, TN, CG, FUSE, FOLD>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + mx_table_bytes(kMxMaxExperts)) !=
         cudaSuccess)
         return EXL3_ERR_CUDA;
@@ -1348,7 +1434,10 @@ static exl3_status launch_mx_tile(int tn, const MxParams &p, const CUtensorMap &
 {
     if constexpr (sizeof(T) == 2)
         if (p.x)
-            return launch_mx<T, 16, 1, true>(p, wmap, xmap, workers, pdl, s);
+            return p.fold ? launch_mx<T, 16, 1, true, true>(p, wmap, xmap, workers, pdl, s)
+                          : launch_mx<T, 16, 1, true>(p, wmap, xmap, workers, pdl, s);
+    if (p.fold)
+        return launch_mx<T, 16, 1, false, true>(p, wmap, xmap, workers, pdl, s);
     switch (tn) {
     case 16: return launch_mx<T, 16, 1>(p, wmap, xmap, workers, pdl, s);
     case 32: return launch_mx<T, 32, 1>(p, wmap, xmap, workers, pdl, s);
@@ -1390,7 +1479,7 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     const int bm = split.bm;
     CUtensorMap wmap, xmap;
     // (with x the tokens' map is not used)
-    if (!code_map(&wmap, wc, experts * n, k / 2, bm) || !code_map(&xmap, x ? wc : xc, x ? n : m, k / 2, tn / cg))
+    if (!code_map(&wmap, wc, experts * n, k / 2, bm) || !code_map(&xmap, x ? wc : xc, x ? n : m, k / 2, (tn / cg) >> split.fold))
         return EXL3_ERR_CUDA;
     MxParams p;
     p.x = x;
@@ -1406,7 +1495,8 @@ static exl3_status run_mx(const uint8_t *xc, const uint8_t *xs, const int32_t *o
     p.rows = m;
     p.n = (int)n;
     p.k = (int)k;
-    p.kb_count = (int)kb_count;
+    p.kb_count = (int)((kb_count + (1 << split.fold) - 1) >> split.fold);
+    p.fold = split.fold;
     p.bm = bm;
     p.experts = (int)experts;
     p.stride = (int)mx4_scale_stride(k);

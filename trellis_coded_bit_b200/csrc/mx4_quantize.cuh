@@ -193,8 +193,8 @@ __device__ __forceinline__ float sticky32(double v)
     return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// A block in fp64, read again (x, signs: the thread's 32 columns).  A call of
-// its own: about one warp in 30 of normal data comes here.
+// A block in fp64, read again (x, signs: the thread's 32 columns), where its
+// scale is in doubt or out of fp32's range.
 template <typename T>
 __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *signs, int *byte)
 {
@@ -236,6 +236,67 @@ __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *sign
         out[c] = unsigned_zeros(codes8(r));
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// The codes in doubt alone (`differ`: nonzero nibbles), each from the exact sum:
+// every group of 4 lanes takes its first one in turn, a lane summing its 32
+// columns with the signs of that row of the Hadamard matrix,
+// (-1)^popcount(row & column).  A call of its own: about one warp in 30 of normal
+// data comes here, nearly always with one code.
+template <typename T>
+__device__ __noinline__ uint4 settle_codes(const T *x, const __half *signs, uint4 code, uint4 differ, int byte)
+{
+    const int lane = threadIdx.x & 31, l = lane & 3, group0 = lane & ~3;
+    for (;;) {
+        const bool mine = (differ.x | differ.y | differ.z | differ.w) != 0;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        if (who == 0)
+            return code;
+        // the group's first lane in doubt, its first code and its scale
+        const uint32_t in_group = (who >> group0) & 15u;
+        const int src = in_group ? __ffs((int)in_group) - 1 : 0;
+        const uint32_t word = differ.x ? differ.x : differ.y ? differ.y : differ.z ? differ.z : differ.w;
+        const int index = differ.x ? 0 : differ.y ? 1 : differ.z ? 2 : 3;
+        const int first = 8 * index + (word ? (__ffs((int)word) - 1) / 4 : 0);
+        const int e = __shfl_sync(0xffffffffu, first, group0 + src);
+        // bit j: the sign of column j of a block in row e (within a block)
+        uint32_t row = 0;
+        row ^= (e & 1) ? 0xaaaaaaaau : 0u;
+        row ^= (e & 2) ? 0xccccccccu : 0u;
+        row ^= (e & 4) ? 0xf0f0f0f0u : 0u;
+        row ^= (e & 8) ? 0xff00ff00u : 0u;
+        row ^= (e & 16) ? 0xffff0000u : 0u;
+        row ^= (__popc(src & l) & 1) ? 0xffffffffu : 0u;
+        double sum = 0.0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+            float f[8], s[8];
+            load8<T>(x + c, f);
+            if (signs)
+                load8<__half>(signs + c, s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double v = signs ? (double)f[j] * (double)s[j] : (double)f[j];
+                sum += (row >> (c + j) & 1u) ? -v : v;
+            }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (mine && l == src) {
+            sum *= 0.088388347648318440550;  // 1/sqrt(128)
+            float r[8] = {sticky32(sum * __longlong_as_double((long long)(1023 + 127 - byte) << 52)), 0.f, 0.f, 0.f,
+                          0.f, 0.f, 0.f, 0.f};
+            const uint32_t q = unsigned_zeros(codes8(r)) & 15u;
+            const int shift = 4 * (e & 7);
+            const uint32_t keep = ~(15u << shift);
+            uint32_t *const c = index == 0 ? &code.x : index == 1 ? &code.y : index == 2 ? &code.z : &code.w;
+            *c = (*c & keep) | (q << shift);
+            differ.x &= index == 0 ? keep : 0xffffffffu;
+            differ.y &= index == 1 ? keep : 0xffffffffu;
+            differ.z &= index == 2 ? keep : 0xffffffffu;
+            differ.w &= index == 3 ? keep : 0xffffffffu;
+        }
+    }
 }
 
 // Columns 32 p + 8 l .. + 7, p = 0 .. 3, of the 128 from x (x and signs: at column
@@ -312,8 +373,11 @@ __device__ __forceinline__ void load_signed(const T *x, const __half *signs, F2 
 // and `slack` is 2^-8 more than that, for the roundings of S and of itself.
 // The block of 32 columns at x (signs: its signs, or null) with the 128-point
 // rotation: codes and scale byte.  The whole warp calls it, 4 consecutive lanes
-// on the consecutive blocks of 128 columns.
-template <typename T>
+// on the consecutive blocks of 128 columns.  SETTLE: only the codes in doubt are
+// summed again (a tenth of the code to fetch, which is what a single call waits
+// for; over many blocks the whole warp's repeat in fp64 is quicker, 21.5 us
+// against 23.3 for 2048 x 8192 fp16).
+template <typename T, bool SETTLE = false>
 __device__ __forceinline__ uint4 quantize_block_rotated(const T *x, const __half *signs, int *out_byte)
 {
     F2 v[16];
@@ -339,13 +403,14 @@ __device__ __forceinline__ uint4 quantize_block_rotated(const T *x, const __half
     int byte = scale_byte32(__float_as_uint(top * s));
     uint4 code = make_uint4(0u, 0u, 0u, 0u);
     // zeros are exact; what leaves fp32's range or the scales' takes fp64
-    bool sure = sum == 0.f;
+    bool sure = sum == 0.f;  // of the scale
+    uint32_t differ[4] = {0u, 0u, 0u, 0u};
     if (!sure && byte >= 1 && byte <= 253 && sum < 1e38f) {
         const float inv = inverse_scale32(byte) * s;
         const float slack = fmaf(0x1.01p-21f * sum, inv, 0x1.01p-20f);
         const float most = top * inv;
         const F2 inv2 = f2(inv, inv);
-        uint32_t out[4], differ = 0;
+        uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float lo[8], hi[8];
@@ -355,14 +420,18 @@ __device__ __forceinline__ uint4 quantize_block_rotated(const T *x, const __half
                 unpack(fma2(v[4 * i + j], inv2, f2(slack, slack)), hi[2 * j], hi[2 * j + 1]);
             }
             const uint32_t a = codes8(lo);
-            differ |= (a ^ codes8(hi)) & 0x77777777u;  // equal magnitudes above 0 have equal signs
+            differ[i] = (a ^ codes8(hi)) & 0x77777777u;  // equal magnitudes above 0 have equal signs
             out[i] = unsigned_zeros(a);
         }
         code = make_uint4(out[0], out[1], out[2], out[3]);
-        sure = differ == 0 && most > 4.f + slack && most < 8.f - slack;
+        sure = most > 4.f + slack && most < 8.f - slack;
     }
+    if (!SETTLE)
+        sure = sure && (differ[0] | differ[1] | differ[2] | differ[3]) == 0;
     if (!__all_sync(0xffffffffu, sure))
         code = quantize_block_fp64<T>(x, signs, &byte);
+    else if (SETTLE && __any_sync(0xffffffffu, (differ[0] | differ[1] | differ[2] | differ[3]) != 0))
+        code = settle_codes<T>(x, signs, code, make_uint4(differ[0], differ[1], differ[2], differ[3]), byte);
     *out_byte = byte;
     return code;
 }
