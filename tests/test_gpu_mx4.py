@@ -390,7 +390,8 @@ def experts_case(rng, counts, k, n, spare=0, low=120, high=127):
 @pytest.mark.parametrize("counts,k,n,spare", [([1], 64, 20, 0), ([0, 3, 0, 0, 1], 256, 130, 2), ([5, 0, 17, 2], 544, 100, 1),
                                               ([40, 1, 0, 90, 16], 512, 256, 0), ([300, 2, 130], 1024, 128, 7),
                                               ([0, 0], 128, 64, 4), ([1] * 40, 256, 48, 0), ([700, 1, 300], 256, 200, 0),
-                                              ([900, 0, 257, 1500, 3, 640], 512, 3000, 5), ([200] * 16, 288, 2600, 0)])
+                                              ([900, 0, 257, 1500, 3, 640], 512, 3000, 5), ([200] * 16, 288, 2600, 0),
+                                              ([3], 2112, 1000, 1), ([2], 4096, 2049, 2), ([100], 4096, 300, 2)])
 def test_experts(counts, k, n, spare):
     rng = np.random.default_rng(sum(counts) + k)
     offsets, x, w = experts_case(rng, counts, k, n, spare)
