@@ -37,7 +37,9 @@
 // 2000).
 //
 // All waits are bounded; a timeout is recorded in the workspace status word,
-// and copies and MMAs in flight are drained before the CTA exits.
+// and copies, MMAs and arrivals in flight are drained before the CTA exits: in the
+// usual case the copying warps wait for the last MMAs on every stage (which read
+// what was copied), after a timeout as mx_settle_pair and the producer say.
 #include <cuda.h>
 #include <math.h>
 
@@ -46,6 +48,7 @@
 #include "exl3_host.h"
 #include "mx4.cuh"
 #include "mx4_quantize.cuh"
+#include "mx4_settle.h"
 #include "tcgen05.cuh"
 
 namespace exl3 {
@@ -117,6 +120,9 @@ struct MxBars {
     uint32_t tmem_slot;
     int epi_abort;
     int ticket;
+    // CG = 2
+    int failed;                  // a role of either CTA stopped early (set in both)
+    uint32_t steps[kMxRoles];    // in the leader: steps that each role has done
 };
 static_assert(sizeof(MxBars) <= 1024, "barrier block");
 
@@ -213,6 +219,59 @@ __device__ __forceinline__ uint32_t leader_addr(uint64_t *bar)
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(leader_addr(bar)) : "memory");
+}
+
+// Stores a word at the place of `at` in the cluster's CTA `rank`; visible there
+// after the next cluster_sync.
+__device__ __forceinline__ void store_in_cta(void *at, uint32_t rank, uint32_t v)
+{
+    asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\nst.shared::cluster.u32 [a], %2;\n}\n" ::"r"(
+                     smem_addr(at)),
+                 "r"(rank), "r"(v)
+                 : "memory");
+}
+
+// A role of the pair (mx4_settle.h) has ended after `steps` steps.
+__device__ __forceinline__ void mx_role_done(MxBars &bars, int role, uint32_t steps)
+{
+    if ((threadIdx.x & 31) == 0)
+        store_in_cta(&bars.steps[role], 0, steps);
+}
+
+// A role stopped before its time: the timeout is recorded, and both CTAs of a
+// pair learn of it.
+template <int CG>
+__device__ __forceinline__ void mx_failed(MxBars &bars, uint32_t *status)
+{
+    record_timeout(status);
+    if constexpr (CG == 2) {
+        store_in_cta(&bars.failed, 0, 1u);
+        store_in_cta(&bars.failed, 1, 1u);
+    }
+}
+
+// The leader's producer warp, when all roles of the pair have ended and one of
+// them early: completes the stages' barriers in place of the roles that stopped
+// and waits until every copy that either CTA began has landed.
+__device__ __forceinline__ void mx_settle_pair(MxBars &bars, uint32_t stages, uint32_t bytes)
+{
+    uint32_t first, end;
+    mx_debt_range(bars.steps, stages, first, end);
+    for (uint32_t i = first; i < end; ++i) {
+        uint64_t *const bar = &bars.full[i % stages];
+        const MxDebt d = mx_debt(bars.steps, i, bytes);
+        if ((threadIdx.x & 31) == 0) {
+            if (d.tx > 0)
+                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(d.tx) : "memory");
+            if (d.tx < 0)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(-d.tx) : "memory");
+            for (uint32_t j = 0; j < d.arrivals; ++j)
+                mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (!warp_wait_uniform(bar, (i / stages) & 1u, kDefaultWaitNs))
+            break;  // (the limit is long enough for all that is in flight)
+    }
 }
 
 // True in one lane of the converged warp.  The MMA issuer runs its loop with
@@ -541,7 +600,7 @@ __device__ __forceinline__ bool mx_epilogue(const MxParams &p, MxBars &bars, con
             }
         }
         if (!ok) {
-            record_timeout(p.status);
+            mx_failed<CG>(bars, p.status);
             *epi_abort = 1;
         }
     }
@@ -812,6 +871,9 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
         mbar_init(&bars.drain, 1);
         bars.epi_abort = 0;
         bars.ticket = 0;
+        bars.failed = 0;
+        for (int r = 0; r < kMxRoles; ++r)
+            bars.steps[r] = 0;
         if (early) {
             first[0] = 0;
             first[1] = nts * tts;
@@ -948,7 +1010,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
             __syncwarp();
             ok = warp_wait_uniform(&bars.drain, 0, kDefaultWaitNs) && ok;
             if (!ok && lane == 0)
-                record_timeout(p.status);
+                mx_failed<CG>(bars, p.status);
         }
     } else if (FUSE && (warp == kMxScaleWarp0 + 1 || warp >= S::kWarps)) {
         // ----------------------------------- quantising a token or two ---
@@ -1088,23 +1150,28 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 }
             }
         }
-        // copies in flight end before the CTA does (the second CTA of a pair
-        // leaves after the first, at the closing barrier).  Stages from s on
-        // were last filled in the round before this one (in round 0: early).
-        // If arrivals are missing, the limit that the first wait runs out of is
-        // long enough for all of them.
-        if (rank == 0) {
+        // Stage st was last filled in this round, or, from s on, in the one before
+        // (in round 0: early).  The CTA leaves when the MMAs have read every fill,
+        // and so all copies have landed and all arrivals on `empty` have come.
+        auto filled = [&](int st) { return st < s || round == 0 ? round : round - 1; };
+        for (int st = 0; st < ST && ok; ++st)
+            if (issued >> st & 1u)
+                ok = warp_wait_uniform(&bars.empty[st], filled(st) & 1u, p.wait_ns);
+        // After a timeout the copies themselves are waited for: in a pair behind
+        // the closing barrier, on a single CTA here.  If arrivals are missing, the
+        // limit that the first wait runs out of is long enough for all of them.
+        if constexpr (CG == 1) {
             bool landed = true;
-            for (int j = 0; j < ST && landed; ++j) {
+            for (int j = 0; j < ST && !ok && landed; ++j) {
                 const int st = s + j < ST ? s + j : s + j - ST;
-                const uint32_t filled = st < s || round == 0 ? round : round - 1;
                 if (issued >> st & 1u)
-                    landed = warp_wait_uniform(&bars.full[st], filled & 1u, kDefaultWaitNs);
+                    landed = warp_wait_uniform(&bars.full[st], filled(st) & 1u, kDefaultWaitNs);
             }
-            ok = ok && landed;
+        } else {
+            mx_role_done(bars, (int)rank, round * ST + (uint32_t)s);
         }
         if (!ok && lane == 0)
-            record_timeout(p.status);
+            mx_failed<CG>(bars, p.status);
     } else if (warp < kMxEpiWarp0) {
         // ------------------------------------------------------ scales ---
         // Lane l of the first warp owns the weights' rows l, l + 32, l + 64 and
@@ -1184,6 +1251,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
         };
         next();
         uint32_t par = 1;
+        uint32_t steps = 0;
         bool ok = true;
         while (seg < sched.segs && ok) {
 #pragma unroll
@@ -1229,6 +1297,7 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                             else
                                 mbar_arrive_leader(&bars.full[s]);
                         }
+                        ++steps;
                         if (++s == ST) {
                             s = 0;
                             par ^= 1u;
@@ -1247,8 +1316,10 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 }
             }
         }
+        if constexpr (CG == 2)
+            mx_role_done(bars, 2 + 2 * (int)rank + half, steps);
         if (!ok && lane == 0)
-            record_timeout(p.status);
+            mx_failed<CG>(bars, p.status);
     } else {
         // ---------------------------------------------------- epilogue ---
         for (int seg = 0; seg < sched.segs; ++seg)
@@ -1258,8 +1329,20 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
 
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2)
-        cluster_sync();  // the other CTA's commits and arrivals have landed, its MMAs are done
+    if constexpr (CG == 2) {
+        // The roles of both CTAs have ended, and with them the MMAs (the leader
+        // waited for them), the stores and arrivals from one CTA in the other.
+        cluster_sync();
+        if (*(volatile int *)&bars.failed) {  // the same in both
+            if (rank == 0 && warp == kMxTmaWarp)
+                mx_settle_pair(bars, ST, kMxABytes + S::kBBytes);
+            cluster_sync();
+        }
+        // The last commit also arrives here, and with it every one before it.
+        if (rank == 1 && warp == kMxMmaWarp && sched.segs > 0 && !warp_wait_uniform(&bars.drain, 0, kDefaultWaitNs) && lane == 0)
+            record_timeout(p.status);
+        __syncwarp();
+    }
     if (warp == kMxMmaWarp) {
         tc_fence_after();
         mx_tmem_dealloc<CG>(bars.tmem_slot);
