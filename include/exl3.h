@@ -374,7 +374,8 @@ int64_t exl3_mx4_scale_stride(int64_t k); /* 16 ceil(k / 512); 0 if k is invalid
  * A block's scale is 2^(floor(log2(largest magnitude)) - 2) (exponent at least
  * -127), elements round to nearest, ties to the even code, magnitudes above 6
  * scales become 6; a block with an infinity or NaN becomes NaN (scale 255,
- * codes 0).  Scaling is exact; codes behind the rotation are those of its
+ * codes 0).  Products with the signs and scaling are exact (a finite product
+ * above fp32's range is finite); codes behind the rotation are those of its
  * fp64 sums, whatever the way to them, so that all calls agree on them.
  */
 exl3_status exl3_mx4_quantize(const void *x, int dtype, const void *signs, int rotate, const int32_t *positions,

@@ -8,7 +8,7 @@
 // that holds an infinity or a NaN gets the scale byte 255 and codes 0.
 //
 // The scaling by a power of two is exact, so without the rotation every code is
-// the definition's.  With it a sum that fp32 rounds across a border of the
+// that of the product with the sign (mx4_quantize.cuh).  With it a sum that fp32 rounds across a border of the
 // 4-bit rounding would put its code off by a whole step of the format, and two
 // ways to the same sum would disagree by that step.  So the rotation runs in
 // fp32 with a bound on its error, and where a value (or a block's largest)
@@ -58,6 +58,22 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int *byte)
     return codes8(r);
 }
 
+// The same in fp64, for products with the signs that fp32 does not hold.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize8_products(const T *x, const __half *signs, int *byte)
+{
+    double v[8];
+    uint64_t top = products8<T>(x, signs, v);
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, (unsigned long long)top, m);
+        top = o > top ? o : top;
+    }
+    const int b = scale_byte64(top);
+    *byte = b;
+    return b == 255 ? 0u : codes8(v, b);
+}
+
 struct Mx4QuantParams {
     const void *x;
     const __half *signs;
@@ -97,7 +113,10 @@ __device__ __forceinline__ void store_scale(const Mx4QuantParams &p, int64_t row
 // Without rotation: a thread takes 8 consecutive columns, 4 threads a block; a
 // warp 32 consecutive groups of the matrix read as one long row (a row is a
 // multiple of 32 columns, so no block straddles two).
-template <typename T>
+// WIDE: there are signs, and a product may be more than fp32 holds: a warp that
+// meets one takes its groups in fp64.  4096 x 8192 bf16 / fp32, us, in a graph behind
+// an L2 flush: no signs 30.7 / 34.8, signs of +-1 34.8 / 37.0, other signs 57 / 57.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams p)
 {
     grid_dep_wait();
@@ -113,17 +132,23 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams 
         int c = 0;
         if (live)
             split_group(g, groups, row, c);
+        const T *const x = (const T *)p.x + (row * groups + c) * 8;
         float v[8];
-        load8<T>((const T *)p.x + (row * groups + c) * 8, v);
+        load8<T>(x, v);
+        uint32_t other = 0;
         if (p.signs) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(p.signs + c * 8);
             float s[8];
-            load8<__half>(p.signs + c * 8, s);
+            unpack16<__half>(raw, s);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] *= s[i];
+            other = WIDE ? other_than_ones(raw) : 0u;
         }
         int byte;
-        const uint32_t code = quantize8(v, &byte);
+        uint32_t code = quantize8(v, &byte);
+        if (WIDE && __any_sync(0xffffffffu, other != 0))
+            code = quantize8_products<T>(x, p.signs + c * 8, &byte);
         if (!live)
             continue;
         for_each_row(p, row, [&](int64_t to) {
@@ -258,9 +283,11 @@ static unsigned mx4_grid(int64_t threads, int block)
 template <typename T>
 static exl3_status launch_quantize(const Mx4QuantParams &p, bool rotate, cudaStream_t s)
 {
-    const cudaError_t e =
-        rotate ? launch_kernel(mx4_rotate_quantize_kernel<T>, dim3(mx4_grid(p.rows * p.blocks, 128)), dim3(128), 0, s, p)
-               : launch_kernel(mx4_quantize_kernel<T>, dim3(mx4_grid(p.rows * p.blocks * 4, 256)), dim3(256), 0, s, p);
+    const dim3 grid(rotate ? mx4_grid(p.rows * p.blocks, 128) : mx4_grid(p.rows * p.blocks * 4, 256));
+    const bool wide = !kExactProducts<T> && p.signs;
+    const cudaError_t e = rotate ? launch_kernel(mx4_rotate_quantize_kernel<T>, grid, dim3(128), 0, s, p)
+                          : wide ? launch_kernel(mx4_quantize_kernel<T, !kExactProducts<T>>, grid, dim3(256), 0, s, p)
+                                 : launch_kernel(mx4_quantize_kernel<T, false>, grid, dim3(256), 0, s, p);
     if (e != cudaSuccess)
         return EXL3_ERR_CUDA;
     return launch_status();

@@ -5,7 +5,13 @@
 // The definition: e = floor(log2(max |v|)) - 2, clamped to [-127, 127]; codes are
 // v 2^-e rounded to nearest, ties to the even code, magnitudes over 6 taken to 6;
 // a block with an infinity or a NaN has the scale byte 255 and codes 0.
+//
+// v is x or x .* signs, the exact products: fp32 holds them for fp16 x (22 bits,
+// 2^-48 .. 2^32) and for signs of +-1; otherwise (fp32 products of 35 bits, bf16
+// products outside fp32's range) a block is taken in fp64.
 #pragma once
+
+#include <type_traits>
 
 #include "dtypes.cuh"
 #include "mx4.cuh"
@@ -64,6 +70,58 @@ __device__ __forceinline__ int scale_byte32(uint32_t bits)
 __device__ __forceinline__ float inverse_scale32(int byte)
 {
     return byte >= 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+// 2^(127 - byte) as fp64.
+__device__ __forceinline__ double inverse_scale64(int byte)
+{
+    return __longlong_as_double((long long)(1023 + 127 - byte) << 52);
+}
+
+// A double as the fp32 value that rounds to 4 bits the same way: truncated,
+// with the last bit set if anything was cut off, so that a value beside a
+// border or a tie stays beside it.
+__device__ __forceinline__ float sticky32(double v)
+{
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Nonzero bits where 8 signs are not +-1.
+__device__ __forceinline__ uint32_t other_than_ones(uint4 s)
+{
+    return ((s.x ^ 0x3c003c00u) | (s.y ^ 0x3c003c00u) | (s.z ^ 0x3c003c00u) | (s.w ^ 0x3c003c00u)) & 0x7fff7fffu;
+}
+
+// Whether fp32 holds the products of any T with any fp16.
+template <typename T>
+constexpr bool kExactProducts = std::is_same<T, __half>::value;
+
+// 8 exact products and their largest magnitude's bits (NaN above infinity).
+template <typename T>
+__device__ __forceinline__ uint64_t products8(const T *x, const __half *signs, double (&v)[8])
+{
+    float f[8], s[8];
+    load8<T>(x, f);
+    load8<__half>(signs, s);
+    uint64_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = (double)f[i] * (double)s[i];
+        const uint64_t a = (uint64_t)__double_as_longlong(v[i]) & 0x7fffffffffffffffull;
+        top = a > top ? a : top;
+    }
+    return top;
+}
+
+__device__ __forceinline__ uint32_t codes8(const double (&v)[8], int byte)
+{
+    const double inv = inverse_scale64(byte);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = sticky32(v[i] * inv);
+    return codes8(r);
 }
 
 // ------------------------------------------------------ with the rotation ---
@@ -184,15 +242,6 @@ __device__ __forceinline__ uint32_t unsigned_zeros(uint32_t code)
     return m | (code & (some << 3));
 }
 
-// A double as the fp32 value that rounds to 4 bits the same way: truncated,
-// with the last bit set if anything was cut off, so that a value beside a
-// border or a tie stays beside it.
-__device__ __forceinline__ float sticky32(double v)
-{
-    const float f = __double2float_rz(v);
-    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
-
 // A block in fp64, read again (x, signs: the thread's 32 columns), where its
 // scale is in doubt or out of fp32's range.
 template <typename T>
@@ -225,7 +274,7 @@ __device__ __noinline__ uint4 quantize_block_fp64(const T *x, const __half *sign
     *byte = b;
     if (b == 255)
         return make_uint4(0u, 0u, 0u, 0u);
-    const double inv = __longlong_as_double((long long)(1023 + 127 - b) << 52);
+    const double inv = inverse_scale64(b);
     uint32_t out[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -284,7 +333,7 @@ __device__ __noinline__ uint4 settle_codes(const T *x, const __half *signs, uint
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (mine && l == src) {
             sum *= 0.088388347648318440550;  // 1/sqrt(128)
-            float r[8] = {sticky32(sum * __longlong_as_double((long long)(1023 + 127 - byte) << 52)), 0.f, 0.f, 0.f,
+            float r[8] = {sticky32(sum * inverse_scale64(byte)), 0.f, 0.f, 0.f,
                           0.f, 0.f, 0.f, 0.f};
             const uint32_t q = unsigned_zeros(codes8(r)) & 15u;
             const int shift = 4 * (e & 7);
@@ -316,8 +365,7 @@ __device__ __forceinline__ void load_signed(const T *x, const __half *signs, F2 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sg[i] = *reinterpret_cast<const uint4 *>(signs + 32 * i);
-                other |= ((sg[i].x ^ 0x3c003c00u) | (sg[i].y ^ 0x3c003c00u) | (sg[i].z ^ 0x3c003c00u) | (sg[i].w ^ 0x3c003c00u)) &
-                         0x7fff7fffu;
+                other |= other_than_ones(sg[i]);
             }
             if (other == 0) {
 #pragma unroll
@@ -436,19 +484,46 @@ __device__ __forceinline__ uint4 quantize_block_rotated(const T *x, const __half
     return code;
 }
 
+// The block of 32 columns at x times the signs there, in fp64.
+template <typename T>
+__device__ __forceinline__ uint4 quantize_block_products(const T *x, const __half *signs, int *out_byte)
+{
+    uint64_t top = 0;
+    double v[8];
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        const uint64_t t = products8<T>(x + i, signs + i, v);
+        top = t > top ? t : top;
+    }
+    const int byte = scale_byte64(top);
+    *out_byte = byte;
+    if (byte == 255)
+        return make_uint4(0u, 0u, 0u, 0u);
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        products8<T>(x + 8 * i, signs + 8 * i, v);
+        out[i] = codes8(v, byte);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // The same without rotation, each lane by itself.
 template <typename T>
 __device__ __forceinline__ uint4 quantize_block(const T *x, const __half *signs, int *out_byte)
 {
     float v[32];
     uint32_t top = 0;  // magnitudes order like their bits, NaN above infinity
+    uint32_t other = 0;
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
         float f[8];
         load8<T>(x + i, f);
         if (signs) {
+            const uint4 raw = *reinterpret_cast<const uint4 *>(signs + i);
             float s[8];
-            load8<__half>(signs + i, s);
+            unpack16<__half>(raw, s);
+            other |= kExactProducts<T> ? 0u : other_than_ones(raw);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 f[j] *= s[j];
@@ -459,6 +534,8 @@ __device__ __forceinline__ uint4 quantize_block(const T *x, const __half *signs,
             top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
         }
     }
+    if (!kExactProducts<T> && other)
+        return quantize_block_products<T>(x, signs, out_byte);
     const int byte = scale_byte32(top);
     *out_byte = byte;
     if (byte == 255)
