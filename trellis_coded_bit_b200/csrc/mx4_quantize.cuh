@@ -316,19 +316,24 @@ __device__ __noinline__ uint4 settle_codes(const T *x, const __half *signs, uint
         row ^= (e & 8) ? 0xff00ff00u : 0u;
         row ^= (e & 16) ? 0xffff0000u : 0u;
         row ^= (__popc(src & l) & 1) ? 0xffffffffu : 0u;
-        double sum = 0.0;
+        // neighbours first, as the butterflies of quantize_block_fp64 add: the same
+        // roundings where the sums are not exact
+        double part[4];
 #pragma unroll
         for (int c = 0; c < 32; c += 8) {
             float f[8], s[8];
+            double v[8];
             load8<T>(x + c, f);
             if (signs)
                 load8<__half>(signs + c, s);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const double v = signs ? (double)f[j] * (double)s[j] : (double)f[j];
-                sum += (row >> (c + j) & 1u) ? -v : v;
+                v[j] = signs ? (double)f[j] * (double)s[j] : (double)f[j];
+                v[j] = (row >> (c + j) & 1u) ? -v[j] : v[j];
             }
+            part[c / 8] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
+        double sum = (part[0] + part[1]) + (part[2] + part[3]);
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (mine && l == src) {
