@@ -482,6 +482,16 @@ def _shape(t, shape, name):
         raise ValueError("%s must be %s, is %s" % (name, " x ".join(str(s) for s in shape), tuple(t.shape)))
 
 
+def _new(like, shape, dtype, stream):
+    """An output on like's device whose memory belongs to the stream that writes
+    it: on another one it could be memory that work queued there still uses, now
+    or when the caller has dropped it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _call(name, device, stream, *args):
     """Calls the library on `stream`, or on the current stream of `device`,
     with that device current."""
@@ -547,11 +557,11 @@ def exl3_mx4_quantize(x, signs=None, rotate=False, positions=None, out_rows=None
     if signs is not None:
         _shape(signs, (k,), "signs")
     if codes is None:
-        codes = x.new_empty((to, k // 2), dtype=torch.uint8)
+        codes = _new(x, (to, k // 2), torch.uint8, stream)
     else:
         _shape(codes, (to, k // 2), "codes")
     if scales is None:
-        scales = x.new_empty((to, stride), dtype=torch.uint8)
+        scales = _new(x, (to, stride), torch.uint8, stream)
     else:
         _shape(scales, (to, stride), "scales")
     _call("exl3_mx4_quantize", device, stream, _arg(x, x.dtype, "x", device), dtype,
@@ -565,7 +575,7 @@ def exl3_mx4_dequantize(codes, scales, dtype=torch.float16, out=None, stream=Non
     """The values of a 4-bit matrix, rows x k, as fp16, bf16 or fp32."""
     (rows,), k = _mx4_operand(codes, scales, 1, "matrix")
     if out is None:
-        out = codes.new_empty((rows, k), dtype=dtype)
+        out = _new(codes, (rows, k), dtype, stream)
     else:
         _shape(out, (rows, k), "out")
     device, dt = _device(out, "out", DTYPES)
@@ -585,7 +595,7 @@ def exl3_mx4_matmul(xc, xs, wc, ws, dtype=torch.float16, y=None, workspace=None,
     if kw != k:
         raise ValueError("x has k = %d, w has %d" % (k, kw))
     if y is None:
-        y = xc.new_empty((m, n), dtype=dtype)
+        y = _new(xc, (m, n), dtype, stream)
     else:
         _shape(y, (m, n), "y")
     device, dt = _device(y, "y", DTYPES)
@@ -613,7 +623,7 @@ def exl3_mx4_linear(x, wc, ws, signs=None, rotate=False, y=None, workspace=None,
     if signs is not None:
         _shape(signs, (k,), "signs")
     if y is None:
-        y = x.new_empty((m, n), dtype=x.dtype)
+        y = _new(x, (m, n), x.dtype, stream)
     else:
         _shape(y, (m, n), "y")
     _call("exl3_mx4_linear", device, stream, _arg(x, x.dtype, "x", device), dt,
@@ -636,7 +646,7 @@ def exl3_mx4_matmul_experts(xc, xs, offsets, wc, ws, dtype=torch.float16, y=None
         raise ValueError("x has k = %d, w has %d" % (k, kw))
     _shape(offsets, (experts + 1,), "offsets")
     if y is None:
-        y = xc.new_empty((rows, n), dtype=dtype)
+        y = _new(xc, (rows, n), dtype, stream)
     else:
         _shape(y, (rows, n), "y")
     device, dt = _device(y, "y", DTYPES)
@@ -660,11 +670,11 @@ def exl3_moe_sort(ids, experts, offsets=None, positions=None, workspace=None, st
     tokens, topk = ids.shape
     device, _ = _device(ids, "ids", (torch.int32,))
     if offsets is None:
-        offsets = ids.new_empty((experts + 1,), dtype=torch.int32)
+        offsets = _new(ids, (experts + 1,), torch.int32, stream)
     else:
         _shape(offsets, (experts + 1,), "offsets")
     if positions is None:
-        positions = ids.new_empty((tokens, topk), dtype=torch.int32)
+        positions = _new(ids, (tokens, topk), torch.int32, stream)
     else:
         _shape(positions, (tokens, topk), "positions")
     _call("exl3_moe_sort", device, stream, _arg(ids, torch.int32, "ids", device), tokens, topk, experts,
@@ -688,7 +698,7 @@ def exl3_moe_gather(x, positions, out=None, out_rows=None, stream=None):
     topk = _topk(positions, tokens)
     device, dt = _device(x, "x", DTYPES)
     if out is None:
-        out = torch.empty((tokens * topk if out_rows is None else int(out_rows), h), dtype=x.dtype, device=x.device)
+        out = _new(x, (tokens * topk if out_rows is None else int(out_rows), h), x.dtype, stream)
     elif out.dim() != 2 or out.shape[1] != h:
         raise ValueError("out must be rows x h")
     _call("exl3_moe_gather", device, stream, _arg(x, x.dtype, "x", device), dt,
@@ -709,7 +719,7 @@ def exl3_moe_combine(ys, positions, weights=None, dtype=None, y=None, stream=Non
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
     if y is None:
-        y = ys.new_empty((tokens, h), dtype=ys.dtype if dtype is None else dtype)
+        y = _new(ys, (tokens, h), ys.dtype if dtype is None else dtype, stream)
     else:
         _shape(y, (tokens, h), "y")
     if y.dtype not in DTYPES or (y.dtype != ys.dtype and ys.dtype != torch.float32):
@@ -733,11 +743,11 @@ def exl3_moe_combine_grad(dy, ys, positions, weights=None, dys=None, dweights=No
     if weights is not None:
         _shape(weights, (tokens, topk), "weights")
     if dys is None:
-        dys = dy.new_empty((rows, h), dtype=dy.dtype)
+        dys = _new(dy, (rows, h), dy.dtype, stream)
     else:
         _shape(dys, (rows, h), "dys")
     if dweights is None:
-        dweights = dy.new_empty((tokens, topk), dtype=torch.float32)
+        dweights = _new(dy, (tokens, topk), torch.float32, stream)
     else:
         _shape(dweights, (tokens, topk), "dweights")
     _call("exl3_moe_combine_grad", device, stream, _arg(dy, dy.dtype, "dy", device),
