@@ -37,9 +37,8 @@
 // 2000).
 //
 // All waits are bounded; a timeout is recorded in the workspace status word,
-// and copies, MMAs and arrivals in flight are drained before the CTA exits: in the
-// usual case the copying warps wait for the last MMAs on every stage (which read
-// what was copied), after a timeout as mx_settle_pair and the producer say.
+// and copies, MMAs and arrivals in flight are drained before the CTA exits (of a
+// pair: by both CTAs, see the end of the producer and of the kernel).
 #include <cuda.h>
 #include <math.h>
 
@@ -1150,24 +1149,26 @@ __global__ void __launch_bounds__(FUSE ? MxTile<TN, CG>::kFuseThreads : MxTile<T
                 }
             }
         }
-        // Stage st was last filled in this round, or, from s on, in the one before
-        // (in round 0: early).  The CTA leaves when the MMAs have read every fill,
-        // and so all copies have landed and all arrivals on `empty` have come.
+        // Copies in flight end before the CTA does.  Stage st was last filled in
+        // this round, or, from s on, in the one before (in round 0: early).
         auto filled = [&](int st) { return st < s || round == 0 ? round : round - 1; };
-        for (int st = 0; st < ST && ok; ++st)
-            if (issued >> st & 1u)
-                ok = warp_wait_uniform(&bars.empty[st], filled(st) & 1u, p.wait_ns);
-        // After a timeout the copies themselves are waited for: in a pair behind
-        // the closing barrier, on a single CTA here.  If arrivals are missing, the
-        // limit that the first wait runs out of is long enough for all of them.
         if constexpr (CG == 1) {
+            // If arrivals are missing, the limit that the first wait runs out of is
+            // long enough for all of them.  (The MMAs and their arrivals: the issuer.)
             bool landed = true;
-            for (int j = 0; j < ST && !ok && landed; ++j) {
+            for (int j = 0; j < ST && landed; ++j) {
                 const int st = s + j < ST ? s + j : s + j - ST;
                 if (issued >> st & 1u)
                     landed = warp_wait_uniform(&bars.full[st], filled(st) & 1u, kDefaultWaitNs);
             }
+            ok = ok && landed;
         } else {
+            // Each CTA waits until the MMAs have read its every fill, and so all
+            // copies of the pair have landed and the arrivals on `empty` have come.
+            // After a timeout the copies are waited for behind the closing barrier.
+            for (int st = 0; st < ST && ok; ++st)
+                if (issued >> st & 1u)
+                    ok = warp_wait_uniform(&bars.empty[st], filled(st) & 1u, p.wait_ns);
             mx_role_done(bars, (int)rank, round * ST + (uint32_t)s);
         }
         if (!ok && lane == 0)
