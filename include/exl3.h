@@ -354,8 +354,10 @@ exl3_status exl3_ldlq(const float *w, const double *h, uint16_t *trellis, float 
  *            16 bytes (the padding is never read as a scale).
  * k, a multiple of 32 (at most 2^22), runs along the sums of a product: a
  * layer's weights are stored with one row per OUTPUT channel (n rows of k).
- * Row counts are 0 .. 2^30; with no rows a call is a no-op.  Types are
- * exl3_dtype.  Pointers, streams and errors as for the calls above.
+ * Rows of x (rows, m) are 0 .. 2^30; with none a call is a no-op.  A product's
+ * n is 1 .. 2^24 (experts * n at most 2^30).  Types are exl3_dtype.  Pointers
+ * (16-byte aligned, the small ones of ids, positions, offsets and weights too),
+ * streams and errors as for the calls above.
  */
 int64_t exl3_mx4_scale_stride(int64_t k); /* 16 ceil(k / 512); 0 if k is invalid */
 
@@ -369,8 +371,8 @@ int64_t exl3_mx4_scale_stride(int64_t k); /* 16 ceil(k / 512); 0 if k is invalid
  *   positions NULL, or int32 [rows][topk]: row r is written to each of the
  *             rows positions[r][j] (exl3_moe_sort's), those outside
  *             [0, out_rows) are skipped; rows that no position names keep
- *             what they hold.  A row may be named only once.  Without
- *             positions topk and out_rows are ignored.
+ *             what they hold.  A row may be named only once.  topk is 1 ..
+ *             1024; without positions it and out_rows are ignored.
  * A block's scale is 2^(floor(log2(largest magnitude)) - 2) (exponent at least
  * -127), elements round to nearest, ties to the even code, magnitudes above 6
  * scales become 6; a block with an infinity or NaN becomes NaN (scale 255,
@@ -384,14 +386,16 @@ exl3_status exl3_mx4_quantize(const void *x, int dtype, const void *signs, int r
 
 /*
  * exl3_mx4_dequantize -- codes and scales to rows x k fp16, bf16 or fp32
- * (exact in fp32; one rounding to the type, fp16 overflows to infinity).
+ * (one rounding to the type: none in fp32, but magnitudes from 2^128 on, which
+ * the scale bytes 253 and 254 reach, are infinity there, as those above 65504 in
+ * fp16 and those that round to 2^128 in bf16).
  */
 exl3_status exl3_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, void *w, int dtype, int64_t rows,
                                 int64_t k, void *stream);
 
 /*
- * exl3_mx4_matmul -- y = x . w^T for 4-bit x (m rows) and w (n rows), any m
- * and n, fp32 accumulation, y m x n fp16, bf16 or fp32 (row-major; one rounding).
+ * exl3_mx4_matmul -- y = x . w^T for 4-bit x (m rows) and w (n rows, at least
+ * one), odd ones too, fp32 accumulation, y m x n fp16, bf16 or fp32 (row-major; one rounding).
  * Few rows are bound by w's bytes, many by the tensor cores; the kernel
  * splits the work evenly over the SMs and adds split sums in a fixed order,
  * so results are deterministic.  `workspace` as for exl3_gemm (zero-filled
@@ -452,7 +456,9 @@ exl3_status exl3_moe_sort(const int32_t *ids, int64_t tokens, int64_t topk, int6
  * exl3_moe_gather -- tokens into that order: xs[positions[t][j]] = x[t], for
  * x tokens x h and xs rows x h of one type.  Positions outside [0, rows) are
  * skipped, rows that no position names keep what they hold, and a row may be
- * named only once.  Its gradient is exl3_moe_combine without weights.
+ * named only once.  Its gradient is exl3_moe_combine without weights.  For this
+ * call and the next two: tokens 0 .. 2^24 (none: a no-op), topk 1 .. 1024, h
+ * 1 .. 2^22, rows 0 .. 2^31.
  */
 exl3_status exl3_moe_gather(const void *x, int dtype, const int32_t *positions, int64_t tokens, int64_t topk,
                             int64_t h, int64_t rows, void *xs, void *stream);
@@ -487,8 +493,8 @@ exl3_status exl3_moe_combine_grad(const void *dy, const void *ys, int dtype, con
  * EXL3_LAUNCH_PDL -- launch exl3_gemv / exl3_gemm kernels with programmatic
  *   dependent launch (CUDA programmatic stream serialization): a kernel may
  *   start while the preceding kernel in the stream is still finishing, and
- *   it begins streaming its WEIGHT operands (trellis, suh, svh; 4-bit w codes
- *   and scales) at once; all
+ *   it begins streaming its WEIGHT operands (trellis, suh, svh; 4-bit w
+ *   codes) at once; all
  *   other reads (x, the workspace) and every write wait until the preceding
  *   kernel has completed and its writes are visible.  Enable it only when the
  *   weights are not written by the kernel launched immediately before on the

@@ -160,8 +160,10 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const Mx4QuantParams 
 }
 
 // A lane per block of 32, 4 lanes a rotation (mx4_quantize.cuh).
-// 2048 x 8192 fp16 in 22 us (2.0 TB/s; its bytes take 6.5 us): bound by issue, 680
-// instructions a warp and 1024 values, half of its cycles with 4 warps a scheduler.
+// 2048 x 8192 fp16 in 22 us (2.0 TB/s; its bytes take 6.5 us, its 680 instructions a
+// warp and 1024 values 10 us of issue): bound by latency.  126 registers leave 4
+// warps a scheduler, each with one block's chain of loads, butterflies and shuffles
+// in flight and, now and then, the fp64 repeat; they issue on half of the cycles.
 template <typename T>
 __global__ void __launch_bounds__(128) mx4_rotate_quantize_kernel(const Mx4QuantParams p)
 {

@@ -1442,8 +1442,8 @@ struct MxSplit {
 // First / second, us: 16 x 4096 x 4096 8.7 / 8.7 (first), 32 x 4096 x 4096 10.4 / 9.2,
 // 64 x 4096 x 4096 12.2 / 9.9, 64 x 4096 x 14336 13.0 / 10.4, 128 x 8192 x 28672 34.7 /
 // 31.1, 129 x 8192 x 8192 22.5 / 15.1, 1 x 4096 x 14336 10.0 / 9.4, 1 x 14336 x 4096
-// 11.4 / 17.4 (first).  First / third: 1 x 2048 x 2048 6.9 / 5.6, 1 x 4096 x 4096 8.5 /
-// 7.4, 1 x 8192 x 8192 11.9 / 10.3; quantising too 8.4 / 6.7, 9.8 / 9.1, 13.3 / 13.3, and 1 x
+// 11.4 / 17.4 (first).  First / third: 1 x 2048 x 2048 7.5 / 5.3, 1 x 4096 x 4096 8.9 /
+// 7.1, 1 x 8192 x 8192 11.6 / 10.0; quantising too 8.1 / 6.4, 10.3 / 8.7, 13.0 / 12.9, and 1 x
 // 14336 x 4096 12.6 / 16.8 (first).
 static MxSplit mx_split(int64_t rows, int64_t n, int kb, int64_t experts, int tn)
 {
