@@ -156,3 +156,18 @@ def test_layer(dtype, m, k, n, rotate):
     xc, xs = (dev(a) for a in mx4.pack(*mx4.quantize(v)))
     want = exl3.exl3_mx4_matmul(xc, xs, wc, wsc, dtype=dtype, workspace=ws)
     assert torch.equal(torch.nan_to_num(y.float(), nan=77.0), torch.nan_to_num(want.float(), nan=77.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:])
+def test_rotated_products_below_normal_numbers(dtype):
+    """One or a few columns that make the block's scale and 120 whose products fp32
+    can only round to multiples of 2^-149, for scales from the smallest on."""
+    rng = np.random.default_rng(8)
+    k, rows = 256, 96
+    x = rng.uniform(-1, 1, (rows, k)) * 2.0 ** -127
+    for r in range(rows):
+        x[r, rng.choice(k, 6, replace=False)] = rng.uniform(1, 2, 6) * 2.0 ** (-122 + r // 4)
+    s = torch.from_numpy(rng.uniform(0.5, 1, k)).half()
+    x = torch.from_numpy(x).to(dtype)
+    codes, scales = exl3.exl3_mx4_quantize(x.cuda(), signs=s.cuda(), rotate=True)
+    same(codes, scales, mx4.rotate(x.double().numpy(), s.double().numpy()))

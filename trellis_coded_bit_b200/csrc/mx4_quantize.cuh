@@ -424,6 +424,11 @@ __device__ __forceinline__ void load_signed(const T *x, const __half *signs, F2 
 // below 8 each: 2^-20.  Together, in units of the scale,
 //     |r - exact| <= 2^-21 S 2^-e / sqrt(128) + 2^-20,
 // and `slack` is 2^-8 more than that, for the roundings of S and of itself.
+// A product with a sign that fp32 holds only below its normal numbers is off by
+// 2^-150 instead: 128 of them, 2^-143, or with kFp32Byte, whose scale is 2^-111,
+// 2^-35 of the scale, which the 2^-8 covers (they are at least 2^-27 of it).
+constexpr int kFp32Byte = 16;
+
 // The block of 32 columns at x (signs: its signs, or null) with the 128-point
 // rotation: codes and scale byte.  The whole warp calls it, 4 consecutive lanes
 // on the consecutive blocks of 128 columns.  SETTLE: only the codes in doubt are
@@ -458,7 +463,7 @@ __device__ __forceinline__ uint4 quantize_block_rotated(const T *x, const __half
     // zeros are exact; what leaves fp32's range or the scales' takes fp64
     bool sure = sum == 0.f;  // of the scale
     uint32_t differ[4] = {0u, 0u, 0u, 0u};
-    if (!sure && byte >= 1 && byte <= 253 && sum < 1e38f) {
+    if (!sure && byte >= kFp32Byte && byte <= 253 && sum < 1e38f) {
         const float inv = inverse_scale32(byte) * s;
         const float slack = fmaf(0x1.01p-21f * sum, inv, 0x1.01p-20f);
         const float most = top * inv;
